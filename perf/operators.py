@@ -70,7 +70,7 @@ def draw(rng):
         d = rng.choice([1152, 2240, 4608, 5600, _log(rng, 33, 12288), _log(rng, 33, 12288)])
         fmt = rng.choice(["bf16", "bf16", "f16", "f32"])
         m = _log(rng, 1, min(65536, 18432 * 12288 // d // (2 if fmt == "f32" else 1)))
-        group = rng.choice([0, 0, _log(rng, 1, m)])
+        group = rng.choice([0, 0, _log(rng, max(1, m // 4096), m)])
         return dict(op=op, m=m, d=d, fmt=fmt, group_rows=group)
     if op in ("w4a4", "linear"):
         k = rng.choice([1152, 2240, 4608, 5600, 32 * _log(rng, 2, 384)])
@@ -90,12 +90,13 @@ def draw(rng):
     kv_heads = rng.choice([1, 2, 4, 8])
     kind = rng.choice(["prompt", "prompt", "chunk", "token"])
     max_k = _log(rng, 1, 8192)
+    causal = rng.random() < 0.7
     max_q = max_k if kind == "prompt" else 1 if kind == "token" else _log(rng, 1, max_k)
     # at most as many pairs of rows and heads as the longest listed prompt has
-    most = 16384 * 16384 * 24 // (max_q * max_k * kv_heads * group)
+    most = 16384 * 16384 * 24 // (max_q * max_k * kv_heads * group) // (1 if causal else 2)
     batch = min(_log(rng, 1, 32), max(1, most), max(1, 262144 // max_k))
     return dict(op="attention", batch=batch, max_q=max_q, max_k=max_k, heads=group * kv_heads,
-                kv_heads=kv_heads, dim=dim, causal=rng.random() < 0.7,
+                kv_heads=kv_heads, dim=dim, causal=causal,
                 fmt=rng.choice(["bf16", "bf16", "f16"]), ragged=rng.random() < 0.7,
                 lengths=rng.randrange(1 << 16))
 
