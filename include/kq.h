@@ -102,6 +102,15 @@ typedef enum {
     KQ_TRANSFORM_FWHT = 4       /* H_d / sqrt(d) over the row */
 } kq_transform;
 
+/* Storage types of the transformer-block operators (layer norm, linear layer,
+ * attention).  Their parameters (weights of the norm, biases) and statistics
+ * are fp32 whatever the storage type. */
+typedef enum kq_format {
+    KQ_BF16 = 0,
+    KQ_F16 = 1,
+    KQ_F32 = 2
+} kq_format;
+
 /* Alignment rules shared by the quantizer entry points:
  *   A, q, sf, y_debug, factors, s, K_expanded: 16-byte aligned;
  *   lda % 8 == 0 (16-byte row pitch), ldq % 16 == 0. */
@@ -285,6 +294,60 @@ KQ_API kq_status kq_bf16_gemm(const uint16_t *a, int64_t lda, const uint16_t *w,
  */
 KQ_API kq_status kq_layer_error(const float *c, int64_t ldc, const float *c_ref, int64_t ldr,
                                 int64_t m, int64_t n, double *out, cudaStream_t stream);
+
+/*
+ * kq_layer_norm -- layer norm of every row, the operator in front of the
+ * quantizer in a transformer block:
+ *     mean = sum x / d,  rstd = 1 / sqrt(sum (x - mean)^2 / d + eps)
+ *     y[i][c] = (x[i][c] - mean) * rstd * weight[g][c] + bias[g][c]
+ * with one row of weight and bias for all rows (g = 0), or one for every
+ * group_rows consecutive rows (g = i / group_rows: the scale and shift of an
+ * adaptive norm, one pair per sample).  All arithmetic is fp32; y is rounded
+ * once.
+ *   x, ldx      device, [m][ldx] in fmt (KQ_BF16, KQ_F16 or KQ_F32)
+ *   m, d        m >= 0, 1 <= d <= 16384 (any d; odd ones too)
+ *   weight      device fp32 [groups][d], or NULL (ones)
+ *   bias        device fp32 [groups][d], or NULL (zeros)
+ *   group_rows  rows that share one row of weight and bias; 0: all of them.
+ *               groups = ceil(m / group_rows), or 1
+ *   eps         >= 0
+ *   y, ldy      device, [m][ldy] in fmt (written, columns < d; not x)
+ *   mean, rstd  device fp32 [m] or NULL: if given, receive the statistics
+ * x, y, weight and bias are 16-byte aligned, and the row pitches of x and y
+ * multiples of 16 bytes (ldx % 8 == 0 for 16-bit types, % 4 for fp32).
+ */
+KQ_API kq_status kq_layer_norm(const void *x, int64_t ldx, kq_format fmt, int64_t m, int64_t d,
+                               const float *weight, const float *bias, int64_t group_rows,
+                               float eps, void *y, int64_t ldy, float *mean, float *rstd,
+                               cudaStream_t stream);
+
+/*
+ * kq_layer_norm_backward -- gradient of kq_layer_norm.  With
+ * z = (x - mean) * rstd and g = dy * weight:
+ *     dx      = rstd * (g - sum(g) / d - z * sum(g z) / d)
+ *     dweight = sum over the group's rows of dy * z
+ *     dbias   = sum over the group's rows of dy
+ *   dy, lddy, x, ldx  device, [m][ld] in fmt
+ *   weight, group_rows, m, d  as in the forward call
+ *   mean, rstd        device fp32 [m], as kq_layer_norm wrote them
+ *   dx, lddx          device, [m][lddx] in fmt (written), or NULL
+ *   dweight, dbias    device fp32 [groups][d] (overwritten), each may be NULL
+ *   workspace         device, kq_layer_norm_backward_bytes() bytes, 16-byte
+ *                     aligned; may be NULL when that is 0 or neither dweight
+ *                     nor dbias is asked for
+ * The sums run in a fixed order: the same inputs give the same bits.  With
+ * m = 0 and group_rows = 0, dweight and dbias are set to zero.
+ * Alignment as in the forward call; dy, dx as x.
+ */
+KQ_API kq_status kq_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                        kq_format fmt, int64_t m, int64_t d, const float *weight,
+                                        int64_t group_rows, const float *mean, const float *rstd,
+                                        void *dx, int64_t lddx, float *dweight, float *dbias,
+                                        void *workspace, cudaStream_t stream);
+
+/* Workspace bytes of kq_layer_norm_backward (0 if none, or if the arguments
+ * are invalid). */
+KQ_API size_t kq_layer_norm_backward_bytes(int64_t m, int64_t d, int64_t group_rows);
 
 /*
  * kq_expand_blocks -- [KQ] Sec. 3.5.1 K1 (the dense 32x32 blocks are kept

@@ -1,0 +1,91 @@
+// C ABI entry points of the transformer-block operators around the quantizer
+// (layer norm): the argument checks, which run before anything is enqueued.
+#include "kq_internal.h"
+
+using namespace kq;
+
+namespace {
+
+constexpr int64_t kMaxRows = 0x7fffffffLL;       // grid and TMA coordinates are 32-bit
+constexpr int64_t kMaxPitch = 1LL << 38;
+constexpr int64_t kMaxNorm = 16384;              // channels a team of threads holds in registers
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A pitch of ld elements of 4 or 2 bytes is a multiple of 16 bytes.
+bool pitch_ok(int64_t ld, kq_format fmt) { return ld % (fmt == KQ_F32 ? 4 : 8) == 0; }
+
+bool norm_shape_ok(int64_t m, int64_t d, int64_t group_rows)
+{
+    return m >= 0 && m <= kMaxRows && d > 0 && d <= kMaxNorm && group_rows >= 0;
+}
+
+int64_t norm_groups(int64_t m, int64_t group_rows)
+{
+    return group_rows == 0 ? 1 : (m + group_rows - 1) / group_rows;
+}
+
+}  // namespace
+
+extern "C" {
+
+kq_status kq_layer_norm(const void *x, int64_t ldx, kq_format fmt, int64_t m, int64_t d,
+                        const float *weight, const float *bias, int64_t group_rows, float eps,
+                        void *y, int64_t ldy, float *mean, float *rstd, cudaStream_t stream)
+{
+    if (fmt != KQ_BF16 && fmt != KQ_F16 && fmt != KQ_F32) return KQ_ERR_LAYOUT;
+    if (!norm_shape_ok(m, d, group_rows) || ldx < d || ldy < d || ldx > kMaxPitch ||
+        ldy > kMaxPitch || !(eps >= 0.f))
+        return KQ_ERR_SHAPE;
+    if (m == 0) return KQ_OK;
+    if (x == nullptr || y == nullptr) return KQ_ERR_NULL;
+    if (!aligned16(x) || !aligned16(y) || !aligned16(weight) || !aligned16(bias) ||
+        !aligned4(mean) || !aligned4(rstd) || !pitch_ok(ldx, fmt) || !pitch_ok(ldy, fmt))
+        return KQ_ERR_ALIGN;
+    return launch_norm_forward(x, ldx, fmt, m, d, weight, bias, group_rows == 0 ? m : group_rows,
+                               eps, y, ldy, mean, rstd, stream);
+}
+
+kq_status kq_layer_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                                 kq_format fmt, int64_t m, int64_t d, const float *weight,
+                                 int64_t group_rows, const float *mean, const float *rstd, void *dx,
+                                 int64_t lddx, float *dweight, float *dbias, void *workspace,
+                                 cudaStream_t stream)
+{
+    if (fmt != KQ_BF16 && fmt != KQ_F16 && fmt != KQ_F32) return KQ_ERR_LAYOUT;
+    if (!norm_shape_ok(m, d, group_rows) || ldx < d || lddy < d || ldx > kMaxPitch ||
+        lddy > kMaxPitch || (dx != nullptr && (lddx < d || lddx > kMaxPitch)))
+        return KQ_ERR_SHAPE;
+    if (!aligned4(dweight) || !aligned4(dbias)) return KQ_ERR_ALIGN;
+    if (m == 0) {
+        // no rows: the one group's sums are zero
+        const size_t bytes = group_rows == 0 ? static_cast<size_t>(d) * sizeof(float) : 0;
+        for (float *p : {dweight, dbias})
+            if (p != nullptr && bytes != 0 && cudaMemsetAsync(p, 0, bytes, stream) != cudaSuccess)
+                return KQ_ERR_CUDA;
+        return KQ_OK;
+    }
+    if (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr) return KQ_ERR_NULL;
+    const bool sums = dweight != nullptr || dbias != nullptr;
+    if (sums && workspace == nullptr && kq_layer_norm_backward_bytes(m, d, group_rows) != 0)
+        return KQ_ERR_NULL;
+    if (!aligned16(dy) || !aligned16(x) || !aligned16(dx) || !aligned16(weight) ||
+        !aligned16(workspace) || !aligned4(mean) || !aligned4(rstd) || !pitch_ok(ldx, fmt) ||
+        !pitch_ok(lddy, fmt) || (dx != nullptr && !pitch_ok(lddx, fmt)))
+        return KQ_ERR_ALIGN;
+    if (dx == nullptr && !sums) return KQ_OK;
+    return launch_norm_backward(dy, lddy, x, ldx, fmt, m, d, weight,
+                                group_rows == 0 ? m : group_rows, mean, rstd, dx, lddx, dweight,
+                                dbias, workspace, stream);
+}
+
+size_t kq_layer_norm_backward_bytes(int64_t m, int64_t d, int64_t group_rows)
+{
+    if (!norm_shape_ok(m, d, group_rows) || m == 0) return 0;
+    const int64_t parts = norm_parts(m, group_rows == 0 ? m : group_rows);
+    if (parts <= 1) return 0;
+    return static_cast<size_t>(norm_groups(m, group_rows)) * static_cast<size_t>(parts) * 2u *
+           static_cast<size_t>(d) * sizeof(float);
+}
+
+}  // extern "C"

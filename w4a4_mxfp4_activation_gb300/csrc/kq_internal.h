@@ -113,6 +113,18 @@ kq_status launch_bf16_gemm(const uint16_t *a, int64_t lda, const uint16_t *w, in
 kq_status launch_layer_error(const float *c, int64_t ldc, const float *r, int64_t ldr, int64_t m,
                              int64_t n, double *out, cudaStream_t stream);
 
+// Layer norm; group_rows > 0.  norm_parts: row slices per group of the
+// backward pass (its workspace is [groups][parts][2][d] fp32 when parts > 1).
+int64_t norm_parts(int64_t m, int64_t group_rows);
+kq_status launch_norm_forward(const void *x, int64_t ldx, kq_format fmt, int64_t m, int64_t d,
+                              const float *weight, const float *bias, int64_t group_rows, float eps,
+                              void *y, int64_t ldy, float *mean, float *rstd, cudaStream_t stream);
+kq_status launch_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
+                               kq_format fmt, int64_t m, int64_t d, const float *weight,
+                               int64_t group_rows, const float *mean, const float *rstd, void *dx,
+                               int64_t lddx, float *dweight, float *dbias, void *workspace,
+                               cudaStream_t stream);
+
 kq_status validate_quant_args(const uint16_t *A, int64_t m, int64_t d, int64_t lda,
                               const uint8_t *q, int64_t ldq, const uint8_t *sf,
                               kq_sf_layout layout, const float *y_debug);

@@ -40,6 +40,7 @@ EXPORTS = (
     "kq_quantize_mxfp4_dual",
     "kq_fwht_quantize_mxfp4", "kq_w4a4_gemm", "kq_bf16_gemm",
     "kq_layer_error", "kq_quantize_mxfp4_shared", "kq_quantize_mxfp4_ex",
+    "kq_layer_norm", "kq_layer_norm_backward", "kq_layer_norm_backward_bytes",
 )
 TESTING_EXPORTS = (
     "kq_quantize_mxfp4_variant", "kq_w4a4_gemm_variant", "kq_test_encode_e2m1",
@@ -117,6 +118,14 @@ def lib() -> ctypes.CDLL:
             L.kq_bf16_gemm.restype = st
             L.kq_layer_error.argtypes = [vp, i64, vp, i64, i64, i64, vp, vp]
             L.kq_layer_error.restype = st
+            f32 = ctypes.c_float
+            L.kq_layer_norm.argtypes = [vp, i64, st, i64, i64, vp, vp, i64, f32, vp, i64, vp, vp, vp]
+            L.kq_layer_norm.restype = st
+            L.kq_layer_norm_backward.argtypes = [vp, i64, vp, i64, st, i64, i64, vp, i64, vp, vp, vp,
+                                                 i64, vp, vp, vp, vp]
+            L.kq_layer_norm_backward.restype = st
+            L.kq_layer_norm_backward_bytes.argtypes = [i64, i64, i64]
+            L.kq_layer_norm_backward_bytes.restype = ctypes.c_size_t
             _lib = L
     return _lib
 
@@ -419,3 +428,114 @@ def kq_layer_error(c, c_ref, out=None, stream=None):
                                 _ptr(out), _stream(stream)),
            "kq_layer_error")
     return out
+
+
+# --- the operators of a transformer block around the quantizer ---------------------
+
+_FORMAT = None
+
+
+def _format(dtype) -> int:
+    """kq_format of a torch dtype (bfloat16, float16 or float32)."""
+    global _FORMAT
+    if _FORMAT is None:
+        import torch
+        _FORMAT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+    try:
+        return _FORMAT[dtype]
+    except KeyError:
+        raise TypeError(f"bfloat16, float16 or float32 expected, got {dtype}") from None
+
+
+def _rows(t, what: str):
+    """A [rows, columns] tensor whose columns are adjacent: its row pitch."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be two-dimensional")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what}: the columns of a row must be adjacent in memory")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), _pitch(t.shape[1], t.dtype))
+
+
+def _pitch(n: int, dtype) -> int:
+    """n rounded up to a row pitch of a multiple of 16 bytes."""
+    unit = 4 if _format(dtype) == 2 else 8
+    return n + (-n) % unit
+
+
+def _empty_rows(m: int, n: int, dtype, device):
+    """[m, n] of ``dtype`` with a row pitch of a multiple of 16 bytes."""
+    import torch
+    ld = _pitch(n, dtype)
+    t = torch.empty((m, ld), dtype=dtype, device=device)
+    return t if ld == n else t[:, :n]
+
+
+def _f32(t, what: str, *shape):
+    """fp32, contiguous, of the given shape (or None): its pointer."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype != torch.float32 or not t.is_contiguous():
+        raise TypeError(f"{what} must be contiguous float32")
+    n = 1
+    for v in shape:
+        n *= v
+    if t.numel() != n:
+        raise ValueError(f"{what} must have shape {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _groups(m: int, group_rows: int) -> int:
+    return 1 if group_rows == 0 else -(-m // max(group_rows, 1))
+
+
+def kq_layer_norm(x, weight=None, bias=None, eps: float = 1e-6, group_rows: int = 0,
+                  stats: bool = False, y=None, stream=None):
+    """Layer norm of the rows of x ([m, d] bfloat16, float16 or float32).
+    weight, bias: fp32 [groups, d] (or [d]), one row for every ``group_rows``
+    rows of x (0: one for all).  Returns y, or (y, mean, rstd) with
+    ``stats=True`` (fp32 [m], for the backward pass)."""
+    import torch
+    m, d = x.shape
+    fmt, ldx = _format(x.dtype), _rows(x, "x")
+    groups = _groups(m, group_rows)
+    if y is None:
+        y = _empty_rows(m, d, x.dtype, x.device)
+    elif y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError("y must have the shape and type of x")
+    mean = rstd = None
+    if stats:
+        mean = torch.empty(m, dtype=torch.float32, device=x.device)
+        rstd = torch.empty(m, dtype=torch.float32, device=x.device)
+    _check(lib().kq_layer_norm(_ptr(x), ldx, fmt, m, d, _f32(weight, "weight", groups, d),
+                               _f32(bias, "bias", groups, d), group_rows, eps, _ptr(y),
+                               _rows(y, "y"), _ptr(mean), _ptr(rstd), _stream(stream)),
+           "kq_layer_norm")
+    return (y, mean, rstd) if stats else y
+
+
+def kq_layer_norm_backward(dy, x, weight, mean, rstd, group_rows: int = 0, dx=None,
+                           stream=None):
+    """Gradient of kq_layer_norm.  Returns (dx, dweight, dbias): dx in the
+    type of x, dweight and dbias fp32 [groups, d]."""
+    import torch
+    m, d = x.shape
+    fmt = _format(x.dtype)
+    if dy.shape != x.shape or dy.dtype != x.dtype:
+        raise ValueError("dy must have the shape and type of x")
+    groups = _groups(m, group_rows)
+    if dx is None:
+        dx = _empty_rows(m, d, x.dtype, x.device)
+    elif dx.shape != x.shape or dx.dtype != x.dtype:
+        raise ValueError("dx must have the shape and type of x")
+    grads = torch.empty((2, groups, d), dtype=torch.float32, device=x.device)
+    nbytes = int(lib().kq_layer_norm_backward_bytes(m, d, group_rows))
+    work = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
+    dweight, dbias = grads[0], grads[1]
+    _check(lib().kq_layer_norm_backward(_ptr(dy), _rows(dy, "dy"), _ptr(x), _rows(x, "x"), fmt, m,
+                                        d, _f32(weight, "weight", groups, d), group_rows,
+                                        _f32(mean, "mean", m), _f32(rstd, "rstd", m), _ptr(dx),
+                                        _rows(dx, "dx"), _ptr(dweight), _ptr(dbias), _ptr(work),
+                                        _stream(stream)),
+           "kq_layer_norm_backward")
+    return dx, dweight, dbias
