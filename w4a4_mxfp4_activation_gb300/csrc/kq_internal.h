@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -58,6 +59,20 @@ kq_status make_tensor_map_2d_f32(CUtensorMap *map, void *base, int64_t rows, int
                                  int64_t ld_elems, uint32_t box_cols, uint32_t box_rows,
                                  CUtensorMapSwizzle swizzle);
 kq_status check_launch();
+
+// Runs a kernel's one-time setup (cudaFuncSetAttribute) once per device.
+struct DeviceOnce {
+    std::once_flag once[64];
+    cudaError_t err[64] = {};
+    template <typename F>
+    kq_status run(F &&setup)
+    {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KQ_ERR_CUDA;
+        std::call_once(once[dev], [&] { err[dev] = setup(); });
+        return err[dev] == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+    }
+};
 
 // The kernels walk tiles in 32-bit arithmetic: row and column tile indices,
 // and the walk's start and stride (at most twice the grid), must fit in int.

@@ -12,9 +12,11 @@
 // dw and db is fp32, and y and dx are rounded once, to nearest even.
 //
 // Both are bound by HBM: x is read once and y written once (forward), x and dy
-// are read once and dx written once (backward).  A row is held by a team of
-// threads in registers, as 16-byte chunks in the storage type, so the second
-// look at it (the centred squares; dx after the two sums) costs no traffic.
+// are read once and dx written once (backward).  A team of 32 to 1024 threads
+// works on a row (forward: on two) in registers, at most three 16-byte chunks a
+// thread for all but the longest rows.  While it does, bulk copies bring its
+// next rows into a ring in shared memory: loads into registers leave no room
+// for a second row, and an SM has to keep about 40 KB in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -34,141 +36,168 @@ struct Chunk {
     static constexpr int kSize = FMT == KQ_F32 ? 4 : 2;
 };
 
+// Values travel as pairs: fp32 additions, products and fused products of two
+// elements issue as one instruction.
 template <int FMT>
-__device__ __forceinline__ void unpack(const uint4 &r, float (&v)[Chunk<FMT>::kN])
+__device__ __forceinline__ void unpack(const uint4 &r, float2 (&v)[Chunk<FMT>::kN / 2])
 {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+    if constexpr (FMT == KQ_F32) {
+        v[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        v[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (FMT == KQ_F32) {
-            v[i] = __uint_as_float(w[i]);
-        } else if constexpr (FMT == KQ_BF16) {
-            v[2 * i] = bf16_lo(w[i]);
-            v[2 * i + 1] = bf16_hi(w[i]);
-        } else {
-            v[2 * i] = f16_lo(w[i]);
-            v[2 * i + 1] = f16_hi(w[i]);
-        }
+        for (int i = 0; i < 4; ++i)
+            v[i] = FMT == KQ_BF16 ? make_float2(bf16_lo(w[i]), bf16_hi(w[i]))
+                                  : make_float2(f16_lo(w[i]), f16_hi(w[i]));
     }
 }
 
 template <int FMT>
-__device__ __forceinline__ uint4 pack(const float (&v)[Chunk<FMT>::kN])
+__device__ __forceinline__ uint4 pack(const float2 (&v)[Chunk<FMT>::kN / 2])
 {
     uint32_t w[4];
+    if constexpr (FMT == KQ_F32) {
+        w[0] = __float_as_uint(v[0].x);
+        w[1] = __float_as_uint(v[0].y);
+        w[2] = __float_as_uint(v[1].x);
+        w[3] = __float_as_uint(v[1].y);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (FMT == KQ_F32) {
-            w[i] = __float_as_uint(v[i]);
-        } else if constexpr (FMT == KQ_BF16) {
-            const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&p);
-        } else {
-            const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&p);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (FMT == KQ_BF16) {
+                const __nv_bfloat162 p = __floats2bfloat162_rn(v[i].x, v[i].y);
+                w[i] = *reinterpret_cast<const uint32_t *>(&p);
+            } else {
+                const __half2 p = __floats2half2_rn(v[i].x, v[i].y);
+                w[i] = *reinterpret_cast<const uint32_t *>(&p);
+            }
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Streaming load: x and dy are read once.
-__device__ __forceinline__ uint4 ldg_stream(const void *p)
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// Zeros in place of the elements of chunk c past column d.  RAG: d is not a
+// multiple of a chunk (a template parameter: as run-time tests these selects
+// cost a third of the kernels' instructions).
+template <bool RAG, int P>
+__device__ __forceinline__ void mask_tail(float2 (&v)[P], int c, int d)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    if constexpr (RAG) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            if (c * 2 * P + 2 * j >= d) v[j].x = 0.f;
+            if (c * 2 * P + 2 * j + 1 >= d) v[j].y = 0.f;
+        }
+    }
 }
 
-// Chunk `c` of a row of d elements: whole 16-byte chunks are loaded as such,
-// the ragged end element by element (zeros past d).
-template <int FMT>
-__device__ __forceinline__ uint4 load_chunk(const uint8_t *row, int c, int d)
+// The elements of a ragged last chunk (out of line: one row in a team's thread
+// takes it, and inlined copies cost instruction cache).
+template <int SIZE>
+__device__ __noinline__ void store_tail(uint8_t *dst, uint4 r, int n)
 {
-    constexpr int N = Chunk<FMT>::kN;
-    if ((c + 1) * N <= d) return ldg_stream(row + 16 * c);
-    uint32_t w[4] = {0, 0, 0, 0};
-    for (int i = 0; c * N + i < d; ++i) {
-        if constexpr (FMT == KQ_F32)
-            w[i] = reinterpret_cast<const uint32_t *>(row)[c * N + i];
-        else
-            w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[c * N + i])
-                         << (16 * (i & 1));
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-template <int FMT>
-__device__ __forceinline__ void store_chunk(uint8_t *row, int c, int d, const uint4 &r)
-{
-    constexpr int N = Chunk<FMT>::kN;
-    if ((c + 1) * N <= d) {
-        stg128_cs(row + 16 * c, r);
-        return;
-    }
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        if (c * N + i >= d) break;
-        if constexpr (FMT == KQ_F32)
-            reinterpret_cast<uint32_t *>(row)[c * N + i] = w[i];
+    for (int i = 0; i < 16 / SIZE; ++i) {
+        if (i >= n) break;
+        if constexpr (SIZE == 4)
+            reinterpret_cast<uint32_t *>(dst)[i] = w[i];
         else
-            reinterpret_cast<uint16_t *>(row)[c * N + i] =
+            reinterpret_cast<uint16_t *>(dst)[i] =
                 static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
     }
 }
 
-// The fp32 parameters of chunk c; `vec`: their row is 16-byte aligned.
-template <int N>
-__device__ __forceinline__ void load_param(const float *p, int c, int d, bool vec, float fill,
-                                           float (&v)[N])
+template <int FMT, bool RAG>
+__device__ __forceinline__ void store_chunk(uint8_t *row, int c, int d, const uint4 &r)
 {
+    constexpr int N = Chunk<FMT>::kN;
+    if (!RAG || (c + 1) * N <= d)
+        stg128_cs(row + 16 * c, r);
+    else
+        store_tail<Chunk<FMT>::kSize>(row + 16 * c, r, d - c * N);
+}
+
+// The fp32 parameters of chunk c; `vec`: their row is 16-byte aligned.
+template <int P>
+__device__ __forceinline__ void load_param(const float *p, int c, int d, bool vec, float fill,
+                                           float2 (&v)[P])
+{
+    constexpr int N = 2 * P;
     if (p == nullptr) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = fill;
+        for (int i = 0; i < P; ++i) v[i] = both(fill);
     } else if (vec && (c + 1) * N <= d) {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(p + c * N + i));
-            v[i] = f.x;
-            v[i + 1] = f.y;
-            v[i + 2] = f.z;
-            v[i + 3] = f.w;
+        for (int i = 0; i < P; i += 2) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(p + c * N + 2 * i));
+            v[i] = make_float2(f.x, f.y);
+            v[i + 1] = make_float2(f.z, f.w);
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = c * N + i < d ? __ldg(p + c * N + i) : 0.f;
+        for (int i = 0; i < P; ++i) {
+            v[i].x = c * N + 2 * i < d ? __ldg(p + c * N + 2 * i) : 0.f;
+            v[i].y = c * N + 2 * i + 1 < d ? __ldg(p + c * N + 2 * i + 1) : 0.f;
+        }
     }
 }
 
-// Sums `v` over a team of TPR threads (whole warps of the block); `red` holds
-// the warps' partial sums of one row, and `buf` alternates from row to row so
-// that one barrier per sum is enough.
+// Barrier of a team of TPR threads; its id is an immediate, because a block
+// that computes ids is charged all 16 barriers and four such fill an SM.
+template <int TPR>
+__device__ __forceinline__ void team_barrier(int team)
+{
+    static_assert(TPR >= 64, "at most two teams a block");
+    if (TPR >= 128 || team == 0)
+        asm volatile("bar.sync 1, %0;" ::"n"(TPR) : "memory");
+    else
+        asm volatile("bar.sync 2, %0;" ::"n"(TPR) : "memory");
+}
+
+// Sums both of v over a team of TPR threads.  The first exchange leaves each
+// half warp with one of the two sums, so that a warp takes five shuffles and
+// not ten; `red` holds the warps' sums of one row, and `buf` alternates from
+// sum to sum so that one barrier per sum is enough.
 template <int TPR>
 __device__ __forceinline__ float2 team_sum(float2 v, float2 *red, int team, int buf)
 {
+    const int lane = threadIdx.x & 31;
+    const bool hi = lane >= 16;
+    const float other = __shfl_xor_sync(0xffffffffu, hi ? v.x : v.y, 16);
+    float a = (hi ? v.y : v.x) + other;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
-    if constexpr (TPR > 32) {
+    for (int o = 8; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if constexpr (TPR == 32) {
+        const float b = __shfl_xor_sync(0xffffffffu, a, 16);
+        return hi ? make_float2(b, a) : make_float2(a, b);
+    } else {
         constexpr int W = TPR / 32;
-        const int warp = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
         float2 *r = red + (team * 2 + buf) * W;
-        if (lane == 0) r[warp] = v;
-        named_barrier(1 + static_cast<uint32_t>(team), TPR);
-        v = lane < W ? r[lane] : make_float2(0.f, 0.f);
+        const int warp = (threadIdx.x % TPR) >> 5;
+        if ((lane & 15) == 0) reinterpret_cast<float *>(r + warp)[lane >> 4] = a;
+        team_barrier<TPR>(team);
+        if constexpr (W <= 8) {
+            v = r[0];
 #pragma unroll
-        for (int o = W / 2; o > 0; o >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            for (int k = 1; k < W; ++k) {
+                const float2 q = r[k];
+                v.x += q.x;
+                v.y += q.y;
+            }
+        } else {
+            v = r[lane & (W - 1)];
+#pragma unroll
+            for (int o = W / 2; o > 0; o >>= 1) {
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+                v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            }
         }
-        v.x = __shfl_sync(0xffffffffu, v.x, 0);
-        v.y = __shfl_sync(0xffffffffu, v.y, 0);
+        return v;
     }
-    return v;
 }
 
 struct NormArgs {
@@ -183,7 +212,9 @@ struct NormArgs {
     int vec;                     // every parameter row is 16-byte aligned
     float eps, inv_d;
     float *mean, *rstd;          // written (forward, may be null) or read (backward)
+    int64_t run;                 // forward: consecutive rows of a team
     int parts;                   // backward: row slices per group
+    int stages;                  // rows in a team's ring
     float *dweight, *dbias;      // backward, [groups][d], may be null
     float *work;                 // backward: [groups][parts][2][d] when parts > 1
 };
@@ -195,148 +226,342 @@ struct Team {
     static constexpr int kRed = TPR > 32 ? kPerBlock * 2 * (TPR / 32) : 1;
 };
 
+// A ring of rows in shared memory, filled by bulk copies that thread 0 of the
+// team issues.  A ragged last chunk is copied whole: what follows it in its
+// row's pitch belongs to the buffer, and is masked.  In the matrix's last row,
+// where nothing need follow, thread 0 stores the chunk's elements itself.
+template <int FMT>
+struct Ring {
+    uint32_t base, bar, row_bytes;
+    int stages;
+
+    __device__ __forceinline__ void put(const uint8_t *src, uint32_t dst, uint32_t whole, int tail,
+                                        uint32_t mbar) const
+    {
+        if (whole) bulk_load(dst, src, whole, mbar);
+        for (int i = 0; i < tail; ++i) {
+            constexpr int SIZE = Chunk<FMT>::kSize;
+            if constexpr (SIZE == 4)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + whole + 4 * i),
+                             "r"(reinterpret_cast<const uint32_t *>(src + whole)[i])
+                             : "memory");
+            else
+                asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + whole + 2 * i),
+                             "h"(reinterpret_cast<const uint16_t *>(src + whole)[i])
+                             : "memory");
+        }
+    }
+    // Fills stage s with a row of x, and one of y after it unless y is null.
+    __device__ __forceinline__ void fill(int s, const uint8_t *x, const uint8_t *y, bool last_row,
+                                         int d) const
+    {
+        constexpr int N = Chunk<FMT>::kN;
+        const uint32_t whole = last_row ? static_cast<uint32_t>(d / N) * 16u : row_bytes;
+        const int tail = last_row ? d % N : 0;
+        const uint32_t mbar = bar + 8 * s, rows = y ? 2u : 1u;
+        const uint32_t dst = base + static_cast<uint32_t>(s) * rows * row_bytes;
+        // the count is raised before the copies can complete; the one arrival
+        // comes last, after this thread's own stores
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(mbar),
+                     "r"(rows * whole)
+                     : "memory");
+        put(x, dst, whole, tail, mbar);
+        if (y) put(y, dst + row_bytes, whole, tail, mbar);
+        mbar_arrive(mbar);
+    }
+    __device__ __forceinline__ void init() const
+    {
+        for (int s = 0; s < stages; ++s) mbar_init(bar + 8 * s, 1);
+        mbar_fence_init();
+    }
+    // Waits for every row from the first one up to `issued` (a wait gave up,
+    // and the block must not leave while copies are in flight).
+    __device__ __noinline__ void drain(int64_t issued) const
+    {
+        for (int64_t i = max(int64_t(0), issued - stages); i < issued; ++i)
+            (void)mbar_wait(bar + 8 * static_cast<int>(i % stages),
+                            static_cast<uint32_t>((i / stages) & 1));
+    }
+};
+
+constexpr int kMaxStages = 4;
+constexpr uint32_t kNan = 0x7FC00000u;
+
 // ---- forward --------------------------------------------------------------------
 
-template <int FMT, int TPR, int VPT>
-__global__ void __launch_bounds__(Team<TPR>::kThreads) norm_forward_kernel(const NormArgs g)
+// A team takes a run of consecutive rows, two at a time: both rows' sums share
+// one reduction, and the parameters (8 bytes a channel, against 2 or 4 of x)
+// are fetched from the caches once for both.  Both rows are in registers before
+// the first reduction; after it their stages are filled again.
+template <int FMT, int TPR, int VPT, bool RAG>
+__global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads)
+    norm_forward_kernel(const NormArgs g)
 {
-    constexpr int N = Chunk<FMT>::kN;
+    constexpr int N = Chunk<FMT>::kN, P = N / 2, PB = Team<TPR>::kPerBlock;
     __shared__ float2 red[Team<TPR>::kRed];
+    __shared__ __align__(8) uint64_t bars[PB][kMaxStages];
+    extern __shared__ __align__(16) uint8_t ring_bytes[];   // [PB][stages][nc * 16]
     const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    const int64_t row = blockIdx.x * static_cast<int64_t>(Team<TPR>::kPerBlock) + team;
+    const int64_t first = (blockIdx.x * static_cast<int64_t>(PB) + team) * g.run;
+    const int64_t rows = min(g.run, g.m - first);           // may be <= 0
+    const int nc = (g.d + N - 1) / N, S = g.stages;
+    Ring<FMT> ring;
+    ring.row_bytes = static_cast<uint32_t>(nc) * 16u;
+    ring.stages = S;
+    ring.base = smem_addr(ring_bytes) + static_cast<uint32_t>(team * S) * ring.row_bytes;
+    ring.bar = smem_addr(&bars[team][0]);
+    if (t == 0) ring.init();
+    __syncthreads();
     grid_dependency_wait();
-    if (row >= g.m) return;
-    const int nc = (g.d + N - 1) / N;
-    const uint8_t *xr = g.x + row * g.xpitch;
-    uint4 raw[VPT];
+    if (rows <= 0) return;
+
+    // thread 0: the next row to copy, and its stage
+    int64_t issued = 0;
+    int fs = 0;
+    const uint8_t *xr = g.x + first * g.xpitch;
+    auto fill = [&] {
+        ring.fill(fs, xr, nullptr, first + issued + 1 == g.m, g.d);
+        xr += g.xpitch;
+        ++issued;
+        fs = fs + 1 == S ? 0 : fs + 1;
+    };
+    if (t == 0)
+        while (issued < S && issued < rows) fill();
+    bool dead = false;                                      // a copy did not arrive in time
+    int s = 0;
+    uint32_t parity = 0;
+    uint8_t *yr = g.y + first * g.ypitch;
+    // the group of the current row, and how many of its rows are left
+    int64_t grp = first / g.group_rows, left = (grp + 1) * g.group_rows - first;
+    for (int64_t i = 0; i < rows; i += 2, yr += 2 * g.ypitch, left -= 2) {
+        while (left <= 0) {
+            ++grp;
+            left += g.group_rows;
+        }
+        const bool two = i + 1 < rows;
+        uint4 raw[2][VPT];
+        if (!dead) dead = !mbar_wait(ring.bar + 8 * s, parity);
+        if (!dead && two) dead = !mbar_wait(ring.bar + 8 * (s + 1), parity);
+        float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = t + i * TPR;
-        raw[i] = c < nc ? load_chunk<FMT>(xr, c, g.d) : make_uint4(0, 0, 0, 0);
-    }
-    float s = 0.f;
+        for (int k = 0; k < VPT; ++k) {
+            const int c = t + k * TPR;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        float v[N];
-        unpack<FMT>(raw[i], v);
+            for (int r = 0; r < 2; ++r) {
+                raw[r][k] = make_uint4(0, 0, 0, 0);
+                if (c < nc) {
+                    // an odd run's missing second row repeats the first
+                    const int st = r && two ? s + 1 : s;
+                    raw[r][k] = lds128(ring.base + static_cast<uint32_t>(st) * ring.row_bytes + 16 * c);
+                    float2 v[P];
+                    unpack<FMT>(raw[r][k], v);
+                    mask_tail<RAG>(v, c, g.d);
 #pragma unroll
-        for (int j = 0; j < N; ++j) s += v[j];
-    }
-    const float mean = team_sum<TPR>(make_float2(s, 0.f), red, team, 0).x * g.inv_d;
-    float q = 0.f;
+                    for (int j = 0; j < P; ++j) sum[r] = __fadd2_rn(sum[r], v[j]);
+                }
+            }
+        }
+        const float2 total =
+            team_sum<TPR>(make_float2(sum[0].x + sum[0].y, sum[1].x + sum[1].y), red, team, 0);
+        if (TPR == 32) __syncwarp();
+        if (t == 0 && !dead)
+            for (int r = 0; r < 2 && issued < rows; ++r) fill();
+        const float mean[2] = {total.x * g.inv_d, total.y * g.inv_d};
+        float2 q[2] = {both(0.f), both(0.f)};
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = t + i * TPR;
-        float v[N];
-        unpack<FMT>(raw[i], v);
+        for (int k = 0; k < VPT; ++k) {
+            const int c = t + k * TPR;
+            if (c < nc) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float e = v[j] - mean;
-            if (c * N + j < g.d) q = fmaf(e, e, q);
+                for (int r = 0; r < 2; ++r) {
+                    float2 v[P];
+                    unpack<FMT>(raw[r][k], v);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) v[j] = __fadd2_rn(v[j], both(-mean[r]));
+                    mask_tail<RAG>(v, c, g.d);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) q[r] = __ffma2_rn(v[j], v[j], q[r]);
+                }
+            }
+        }
+        const float2 var =
+            team_sum<TPR>(make_float2(q[0].x + q[0].y, q[1].x + q[1].y), red, team, 1);
+        // rsqrtf is within 2 ulp, and its few instructions run in every thread
+        float rstd[2] = {rsqrtf(var.x * g.inv_d + g.eps), rsqrtf(var.y * g.inv_d + g.eps)};
+        if (dead) rstd[0] = rstd[1] = __uint_as_float(kNan);
+        const int64_t row = first + i;
+        const bool same = left > 1;
+        const float *w = g.weight ? g.weight + grp * g.d : nullptr;
+        const float *b = g.bias ? g.bias + grp * g.d : nullptr;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = t + k * TPR;
+            if (c < nc) {
+                float2 wv[P], bv[P];
+                load_param<P>(w, c, g.d, g.vec, 1.f, wv);
+                load_param<P>(b, c, g.d, g.vec, 0.f, bv);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    if (r == 1 && !two) break;
+                    if (r == 1 && !same) {
+                        load_param<P>(w ? w + g.d : nullptr, c, g.d, g.vec, 1.f, wv);
+                        load_param<P>(b ? b + g.d : nullptr, c, g.d, g.vec, 0.f, bv);
+                    }
+                    float2 v[P];
+                    unpack<FMT>(raw[r][k], v);
+#pragma unroll
+                    for (int j = 0; j < P; ++j) {
+                        const float2 z = __fmul2_rn(__fadd2_rn(v[j], both(-mean[r])), both(rstd[r]));
+                        v[j] = __ffma2_rn(z, wv[j], bv[j]);
+                    }
+                    store_chunk<FMT, RAG>(yr + r * g.ypitch, c, g.d, pack<FMT>(v));
+                }
+            }
+        }
+        if (t < 2 && i + t < rows) {
+            if (g.mean) g.mean[row + t] = mean[t];
+            if (g.rstd) g.rstd[row + t] = rstd[t];
+        }
+        s += 2;
+        if (s >= S) {
+            s = 0;
+            parity ^= 1;
         }
     }
-    const float var = team_sum<TPR>(make_float2(q, 0.f), red, team, 1).x * g.inv_d;
-    const float rstd = 1.0f / sqrtf(var + g.eps);
-    const int64_t grp = row / g.group_rows;
-    const float *w = g.weight ? g.weight + grp * g.d : nullptr;
-    const float *b = g.bias ? g.bias + grp * g.d : nullptr;
-    uint8_t *yr = g.y + row * g.ypitch;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int c = t + i * TPR;
-        if (c < nc) {
-            float v[N], wv[N], bv[N];
-            unpack<FMT>(raw[i], v);
-            load_param<N>(w, c, g.d, g.vec, 1.f, wv);
-            load_param<N>(b, c, g.d, g.vec, 0.f, bv);
-#pragma unroll
-            for (int j = 0; j < N; ++j) v[j] = fmaf((v[j] - mean) * rstd, wv[j], bv[j]);
-            store_chunk<FMT>(yr, c, g.d, pack<FMT>(v));
-        }
-    }
-    if (t == 0) {
-        if (g.mean) g.mean[row] = mean;
-        if (g.rstd) g.rstd[row] = rstd;
-    }
+    if (t == 0 && dead) ring.drain(issued);
 }
 
 // ---- backward -------------------------------------------------------------------
 
-// A block takes slice p of group gi: teams walk its rows, keep the columns'
-// sums of dy * z and dy in registers, and add them up at the end (in team
-// order: the result does not depend on timing).
-template <int FMT, int TPR, int VPT>
-__global__ void __launch_bounds__(Team<TPR>::kThreads) norm_backward_kernel(const NormArgs g)
+// A block takes slice p of group gi; its teams walk the rows of the slice.  The
+// group's weights and the columns' sums of dy * z and dy stay in registers; the
+// teams' sums are added in team order at the end, so the result does not depend
+// on timing.  The saved statistics of the next 32 rows are fetched by the lanes
+// of each warp at once: one load a row would put its latency into every row.
+template <int FMT, int TPR, int VPT, bool RAG>
+__global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads)
+    norm_backward_kernel(const NormArgs g)
 {
-    constexpr int N = Chunk<FMT>::kN, PB = Team<TPR>::kPerBlock;
+    constexpr int N = Chunk<FMT>::kN, P = N / 2, PB = Team<TPR>::kPerBlock;
     __shared__ float2 red[Team<TPR>::kRed];
-    extern __shared__ float sums[];              // [2][d], PB > 1 only
-    const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    __shared__ __align__(8) uint64_t bars[PB][kMaxStages];
+    extern __shared__ __align__(16) uint8_t ring_bytes[];   // [PB][stages][2][nc * 16]
+    const int team = threadIdx.x / TPR, t = threadIdx.x % TPR, lane = threadIdx.x & 31;
     const int64_t gi = blockIdx.x / static_cast<unsigned>(g.parts);
     const int p = static_cast<int>(blockIdx.x % static_cast<unsigned>(g.parts));
-    const int64_t first = gi * g.group_rows, last = min(g.m, first + g.group_rows);
-    const int nc = (g.d + N - 1) / N;
-    const float *w = g.weight ? g.weight + gi * g.d : nullptr;
-    float aw[VPT][N], ab[VPT][N];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int j = 0; j < N; ++j) aw[i][j] = ab[i][j] = 0.f;
+    const int64_t last = min(g.m, (gi + 1) * g.group_rows);
+    const int64_t first = gi * g.group_rows + static_cast<int64_t>(p) * PB + team;
+    const int64_t step = static_cast<int64_t>(g.parts) * PB;
+    const int64_t rows = first < last ? (last - first + step - 1) / step : 0;
+    const int nc = (g.d + N - 1) / N, S = g.stages;
+    Ring<FMT> ring;
+    ring.row_bytes = static_cast<uint32_t>(nc) * 16u;
+    ring.stages = S;
+    ring.base = smem_addr(ring_bytes) + static_cast<uint32_t>(team * S) * 2u * ring.row_bytes;
+    ring.bar = smem_addr(&bars[team][0]);
+    if (t == 0) ring.init();
+    __syncthreads();
     grid_dependency_wait();
-    int buf = 0;
-    for (int64_t row = first + static_cast<int64_t>(p) * PB + team; row < last;
-         row += static_cast<int64_t>(g.parts) * PB, buf ^= 1) {
+
+    // thread 0: the next row to copy, and its stage
+    int64_t issued = 0;
+    int fs = 0;
+    const uint8_t *xr = g.x + first * g.xpitch, *dyr = g.dy + first * g.dypitch;
+    auto fill = [&] {
+        ring.fill(fs, xr, dyr, first + issued * step + 1 == g.m, g.d);
+        xr += step * g.xpitch;
+        dyr += step * g.dypitch;
+        ++issued;
+        fs = fs + 1 == S ? 0 : fs + 1;
+    };
+    if (t == 0)
+        while (issued < S && issued < rows) fill();
+
+    float2 wv[VPT][P], aw[VPT][P], ab[VPT][P];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int c = t + k * TPR;
+#pragma unroll
+        for (int j = 0; j < P; ++j) wv[k][j] = aw[k][j] = ab[k][j] = both(0.f);
+        if (c < nc) load_param<P>(g.weight ? g.weight + gi * g.d : nullptr, c, g.d, g.vec, 1.f, wv[k]);
+    }
+    float mean32 = 0.f, rstd32 = 0.f;           // of row 32 (i / 32) + lane of this team
+    int s = 0, buf = 0;
+    uint32_t parity = 0;
+    bool dead = false;                          // a copy did not arrive in time
+    uint8_t *yr = g.y + first * g.ypitch;
+    for (int64_t i = 0; i < rows; ++i, yr += step * g.ypitch) {
+        if ((i & 31) == 0 && i + lane < rows) {
+            mean32 = __ldg(g.mean + first + (i + lane) * step);
+            rstd32 = __ldg(g.rstd + first + (i + lane) * step);
+        }
+        float mean = __shfl_sync(0xffffffffu, mean32, static_cast<int>(i & 31));
+        const float rstd = __shfl_sync(0xffffffffu, rstd32, static_cast<int>(i & 31));
+        if (!dead) dead = !mbar_wait(ring.bar + 8 * s, parity);
+        if (dead) mean = __uint_as_float(kNan);
+        const uint32_t sx = ring.base + static_cast<uint32_t>(s) * 2u * ring.row_bytes;
+        const uint32_t sd = sx + ring.row_bytes;
         uint4 rx[VPT], rd[VPT];
+        // dy and z of chunk k; zeros past column d
+        auto chunk = [&](int k, float2(&dy)[P], float2(&z)[P]) {
+            unpack<FMT>(rx[k], z);
+            unpack<FMT>(rd[k], dy);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = t + i * TPR;
-            rx[i] = c < nc ? load_chunk<FMT>(g.x + row * g.xpitch, c, g.d) : make_uint4(0, 0, 0, 0);
-            rd[i] = c < nc ? load_chunk<FMT>(g.dy + row * g.dypitch, c, g.d) : make_uint4(0, 0, 0, 0);
-        }
-        const float mean = __ldg(g.mean + row), rstd = __ldg(g.rstd + row);
-        float2 s = make_float2(0.f, 0.f);
+            for (int j = 0; j < P; ++j)
+                z[j] = __fmul2_rn(__fadd2_rn(z[j], both(-mean)), both(rstd));
+            mask_tail<RAG>(z, t + k * TPR, g.d);
+            mask_tail<RAG>(dy, t + k * TPR, g.d);
+        };
+        float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int c = t + i * TPR;
+        for (int k = 0; k < VPT; ++k) {
+            const int c = t + k * TPR;
+            rx[k] = rd[k] = make_uint4(0, 0, 0, 0);
             if (c < nc) {
-                float x[N], dy[N], wv[N];
-                unpack<FMT>(rx[i], x);
-                unpack<FMT>(rd[i], dy);
-                load_param<N>(w, c, g.d, g.vec, 1.f, wv);
+                rx[k] = lds128(sx + 16 * c);
+                rd[k] = lds128(sd + 16 * c);
+                float2 dy[P], z[P];
+                chunk(k, dy, z);
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    // past d: dy = 0, and z must not turn it into a NaN
-                    const float z = c * N + j < g.d ? (x[j] - mean) * rstd : 0.f;
-                    const float gr = dy[j] * wv[j];
-                    s.x += gr;
-                    s.y = fmaf(gr, z, s.y);
-                    aw[i][j] = fmaf(dy[j], z, aw[i][j]);
-                    ab[i][j] += dy[j];
+                for (int j = 0; j < P; ++j) {
+                    const float2 gr = __fmul2_rn(dy[j], wv[k][j]);
+                    s1 = __fadd2_rn(s1, gr);
+                    s2 = __ffma2_rn(gr, z[j], s2);
+                    aw[k][j] = __ffma2_rn(dy[j], z[j], aw[k][j]);
+                    ab[k][j] = __fadd2_rn(ab[k][j], dy[j]);
                 }
             }
         }
-        s = team_sum<TPR>(s, red, team, buf);
+        const float2 sum = team_sum<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red, team, buf);
+        if (TPR == 32) __syncwarp();
+        // this row's stage: the row is in registers
+        if (t == 0 && issued < rows && !dead) fill();
         if (g.y) {
-            const float c1 = s.x * g.inv_d, c2 = s.y * g.inv_d;
+            // rstd * (g - sum(g) / d - z * sum(g z) / d)
+            const float2 c1 = both(-sum.x * g.inv_d), c2 = both(-sum.y * g.inv_d);
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int c = t + i * TPR;
+            for (int k = 0; k < VPT; ++k) {
+                const int c = t + k * TPR;
                 if (c < nc) {
-                    float x[N], dy[N], wv[N];
-                    unpack<FMT>(rx[i], x);
-                    unpack<FMT>(rd[i], dy);
-                    load_param<N>(w, c, g.d, g.vec, 1.f, wv);
+                    float2 dy[P], z[P];
+                    chunk(k, dy, z);
 #pragma unroll
-                    for (int j = 0; j < N; ++j) {
-                        const float z = (x[j] - mean) * rstd;
-                        x[j] = rstd * (fmaf(dy[j], wv[j], -c1) - z * c2);
-                    }
-                    store_chunk<FMT>(g.y + row * g.ypitch, c, g.d, pack<FMT>(x));
+                    for (int j = 0; j < P; ++j)
+                        z[j] = __fmul2_rn(both(rstd), __ffma2_rn(z[j], c2, __ffma2_rn(dy[j], wv[k][j], c1)));
+                    store_chunk<FMT, RAG>(yr, c, g.d, pack<FMT>(z));
                 }
             }
+        }
+        buf ^= 1;
+        if (++s == S) {
+            s = 0;
+            parity ^= 1;
         }
     }
+    if (t == 0 && dead) ring.drain(issued);
     if (g.dweight == nullptr && g.dbias == nullptr) return;
+    __syncthreads();
+    float *sums = reinterpret_cast<float *>(ring_bytes);      // [2][d], PB > 1 only
     float *ow, *ob;
     if (g.parts > 1) {
         ow = g.work + (gi * g.parts + p) * 2 * static_cast<int64_t>(g.d);
@@ -353,7 +578,8 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads) norm_backward_kernel(cons
                 for (int j = 0; j < N; ++j) {
                     const int col = (t + i * TPR) * N + j;
                     if (col < g.d) {
-                        float a = aw[i][j], b = ab[i][j];
+                        float a = j & 1 ? aw[i][j / 2].y : aw[i][j / 2].x;
+                        float b = j & 1 ? ab[i][j / 2].y : ab[i][j / 2].x;
                         if (k > 0) {
                             a += sums[col];
                             b += sums[g.d + col];
@@ -373,73 +599,117 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads) norm_backward_kernel(cons
     }
 }
 
-// dw and db from the slices' sums, in slice order.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const NormArgs g, int64_t groups)
+// dw and db from the slices' sums.  A block takes 32 neighbouring columns; its
+// 16 warps take every 16th slice each, and the warps' sums are added in order.
+__global__ void __launch_bounds__(512) norm_reduce_kernel(const NormArgs g)
 {
+    __shared__ float part[16][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cols = 2 * g.d, per = (cols + 31) / 32;
+    const int64_t gi = blockIdx.x / static_cast<unsigned>(per);
+    const int col = static_cast<int>(blockIdx.x % static_cast<unsigned>(per)) * 32 + lane;
     grid_dependency_wait();
-    const int64_t total = groups * 2 * g.d;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const int64_t gi = i / (2 * g.d);
-        const int64_t col = i % (2 * g.d);
+    float s = 0.f;
+    if (col < cols) {
+        const float *w = g.work + gi * g.parts * cols + col;
+#pragma unroll 8
+        for (int p = warp; p < g.parts; p += 16) s += w[static_cast<int64_t>(p) * cols];
+    }
+    part[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && col < cols) {
+        s = part[0][lane];
+#pragma unroll
+        for (int k = 1; k < 16; ++k) s += part[k][lane];
         float *out = col < g.d ? g.dweight : g.dbias;
-        if (out == nullptr) continue;
-        const float *w = g.work + gi * g.parts * 2 * g.d + col;
-        float s = 0.f;
-        for (int p = 0; p < g.parts; ++p) s += w[p * 2ll * g.d];
-        out[gi * g.d + (col < g.d ? col : col - g.d)] = s;
+        if (out) out[gi * g.d + (col < g.d ? col : col - g.d)] = s;
     }
 }
 
-template <int FMT, int TPR, int VPT>
-kq_status forward_t(const NormArgs &g, cudaStream_t stream)
+constexpr int kSmemMost = 224 * 1024;
+
+// A kernel's setup and the stages of its ring: as many as fit the share of
+// shared memory of a block where an SM holds 512 threads, 4 at most.
+template <int FMT, int TPR, typename Kernel>
+kq_status ring_setup(Kernel kern, DeviceOnce &once, NormArgs &g, int rows_per_stage, int &stage)
 {
-    constexpr int PB = Team<TPR>::kPerBlock;
-    const int64_t blocks = (g.m + PB - 1) / PB;
-    return launch_pdl(norm_forward_kernel<FMT, TPR, VPT>, static_cast<int>(blocks),
-                      Team<TPR>::kThreads, 0, stream, g);
+    const kq_status st = once.run([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+    });
+    constexpr int kResident = std::max(1, 512 / Team<TPR>::kThreads);
+    const int nc = (g.d + Chunk<FMT>::kN - 1) / Chunk<FMT>::kN;
+    stage = Team<TPR>::kPerBlock * rows_per_stage * 16 * nc;
+    g.stages = std::min(kMaxStages, kSmemMost / kResident / stage);
+    return st;
 }
 
-// A team is the smallest that holds a row in four chunks a thread.
-template <int FMT>
-kq_status forward_f(const NormArgs &g, cudaStream_t stream)
+template <int FMT, int TPR, int VPT, bool RAG>
+kq_status forward_t(NormArgs &g, cudaStream_t stream)
+{
+    constexpr int PB = Team<TPR>::kPerBlock, kResident = std::max(1, 512 / Team<TPR>::kThreads);
+    auto kern = norm_forward_kernel<FMT, TPR, VPT, RAG>;
+    static DeviceOnce once;
+    int stage;
+    const kq_status st = ring_setup<FMT, TPR>(kern, once, g, 1, stage);
+    if (st != KQ_OK) return st;
+    g.stages &= ~1;                                  // rows go two at a time
+    // one wave of teams, an even number of rows each
+    const int64_t teams = static_cast<int64_t>(152) * kResident * PB;
+    g.run = std::max<int64_t>(1, (g.m + teams - 1) / teams);
+    if (g.run > 1) g.run += g.run & 1;
+    const int64_t blocks = (g.m + g.run * PB - 1) / (g.run * PB);
+    return launch_pdl(kern, static_cast<int>(blocks), Team<TPR>::kThreads,
+                      static_cast<size_t>(g.stages * stage), stream, g);
+}
+
+// A team is the smallest that holds a row in three chunks a thread.
+template <int FMT, bool RAG>
+kq_status forward_f(NormArgs &g, cudaStream_t stream)
 {
     const int nc = (g.d + Chunk<FMT>::kN - 1) / Chunk<FMT>::kN;
-    if (nc <= 64) return forward_t<FMT, 32, 2>(g, stream);
-    if (nc <= 160) return forward_t<FMT, 32, 5>(g, stream);
-    if (nc <= 256) return forward_t<FMT, 64, 4>(g, stream);
-    if (nc <= 512) return forward_t<FMT, 128, 4>(g, stream);
-    if (nc <= 1024) return forward_t<FMT, 256, 4>(g, stream);
-    if (nc <= 2048) return forward_t<FMT, 512, 4>(g, stream);
-    if constexpr (FMT == KQ_F32) return forward_t<FMT, 1024, 4>(g, stream);
+    if (nc <= 96) return forward_t<FMT, 32, 3, RAG>(g, stream);
+    if (nc <= 192) return forward_t<FMT, 64, 3, RAG>(g, stream);
+    if (nc <= 384) return forward_t<FMT, 128, 3, RAG>(g, stream);
+    if (nc <= 768) return forward_t<FMT, 256, 3, RAG>(g, stream);
+    if (nc <= 1536) return forward_t<FMT, 512, 3, RAG>(g, stream);
+    if (nc <= 2048) return forward_t<FMT, 512, 4, RAG>(g, stream);
+    if constexpr (FMT == KQ_F32) return forward_t<FMT, 1024, 4, RAG>(g, stream);
     return KQ_ERR_SHAPE;
 }
 
-template <int FMT, int TPR, int VPT>
-kq_status backward_t(const NormArgs &g, int64_t groups, cudaStream_t stream)
+// Row slices per group of the backward pass: four blocks of 128 threads for
+// each of the 152 SMs in all, fewer where rows are few.
+constexpr int64_t kNormParts = 608;
+
+template <int FMT, int TPR, int VPT, bool RAG>
+kq_status backward_t(NormArgs &g, int64_t groups, cudaStream_t stream)
 {
-    const size_t smem = Team<TPR>::kPerBlock > 1 ? 2 * sizeof(float) * static_cast<size_t>(g.d) : 0;
-    return launch_pdl(norm_backward_kernel<FMT, TPR, VPT>, static_cast<int>(groups * g.parts),
-                      Team<TPR>::kThreads, smem, stream, g);
+    constexpr int PB = Team<TPR>::kPerBlock, kResident = std::max(1, 512 / Team<TPR>::kThreads);
+    auto kern = norm_backward_kernel<FMT, TPR, VPT, RAG>;
+    static DeviceOnce once;
+    int stage;
+    const kq_status st = ring_setup<FMT, TPR>(kern, once, g, 2, stage);
+    if (st != KQ_OK) return st;
+    g.parts = static_cast<int>(
+        std::min<int64_t>(g.parts, std::max<int64_t>(1, kResident * 152 / groups)));
+    const int sums = PB > 1 ? 2 * static_cast<int>(sizeof(float)) * g.d : 0;
+    return launch_pdl(kern, static_cast<int>(groups * g.parts), Team<TPR>::kThreads,
+                      static_cast<size_t>(std::max(g.stages * stage, sums)), stream, g);
 }
 
-template <int FMT>
-kq_status backward_f(const NormArgs &g, int64_t groups, cudaStream_t stream)
+template <int FMT, bool RAG>
+kq_status backward_f(NormArgs &g, int64_t groups, cudaStream_t stream)
 {
     const int nc = (g.d + Chunk<FMT>::kN - 1) / Chunk<FMT>::kN;
-    if (nc <= 64) return backward_t<FMT, 32, 2>(g, groups, stream);
-    if (nc <= 128) return backward_t<FMT, 32, 4>(g, groups, stream);
-    if (nc <= 192) return backward_t<FMT, 64, 3>(g, groups, stream);
-    if (nc <= 384) return backward_t<FMT, 128, 3>(g, groups, stream);
-    if (nc <= 768) return backward_t<FMT, 256, 3>(g, groups, stream);
-    if (nc <= 1536) return backward_t<FMT, 512, 3>(g, groups, stream);
-    if (nc <= 2048) return backward_t<FMT, 512, 4>(g, groups, stream);
-    if constexpr (FMT == KQ_F32) return backward_t<FMT, 1024, 4>(g, groups, stream);
+    if (nc <= 96) return backward_t<FMT, 32, 3, RAG>(g, groups, stream);
+    if (nc <= 192) return backward_t<FMT, 64, 3, RAG>(g, groups, stream);
+    if (nc <= 384) return backward_t<FMT, 128, 3, RAG>(g, groups, stream);
+    if (nc <= 768) return backward_t<FMT, 256, 3, RAG>(g, groups, stream);
+    if (nc <= 1536) return backward_t<FMT, 512, 3, RAG>(g, groups, stream);
+    if (nc <= 2048) return backward_t<FMT, 512, 4, RAG>(g, groups, stream);
+    if constexpr (FMT == KQ_F32) return backward_t<FMT, 1024, 4, RAG>(g, groups, stream);
     return KQ_ERR_SHAPE;
 }
-
-// Row slices per group of the backward pass: about two blocks for each of the
-// 152 SMs in all, no slice without a row.
-constexpr int64_t kNormParts = 304;
 
 }  // namespace
 
@@ -473,9 +743,10 @@ kq_status launch_norm_forward(const void *x, int64_t ldx, kq_format fmt, int64_t
     g.inv_d = 1.0f / static_cast<float>(d);
     g.mean = mean;
     g.rstd = rstd;
-    if (fmt == KQ_BF16) return forward_f<KQ_BF16>(g, stream);
-    if (fmt == KQ_F16) return forward_f<KQ_F16>(g, stream);
-    return forward_f<KQ_F32>(g, stream);
+    const bool rag = d % (16 / size) != 0;
+    if (fmt == KQ_BF16) return rag ? forward_f<KQ_BF16, true>(g, stream) : forward_f<KQ_BF16, false>(g, stream);
+    if (fmt == KQ_F16) return rag ? forward_f<KQ_F16, true>(g, stream) : forward_f<KQ_F16, false>(g, stream);
+    return rag ? forward_f<KQ_F32, true>(g, stream) : forward_f<KQ_F32, false>(g, stream);
 }
 
 kq_status launch_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
@@ -507,14 +778,16 @@ kq_status launch_norm_backward(const void *dy, int64_t lddy, const void *x, int6
     g.dweight = dweight;
     g.dbias = dbias;
     g.work = static_cast<float *>(workspace);
-    st = fmt == KQ_BF16  ? backward_f<KQ_BF16>(g, groups, stream)
-         : fmt == KQ_F16 ? backward_f<KQ_F16>(g, groups, stream)
-                         : backward_f<KQ_F32>(g, groups, stream);
+    const bool rag = d % (16 / size) != 0;
+    if (fmt == KQ_BF16)
+        st = rag ? backward_f<KQ_BF16, true>(g, groups, stream) : backward_f<KQ_BF16, false>(g, groups, stream);
+    else if (fmt == KQ_F16)
+        st = rag ? backward_f<KQ_F16, true>(g, groups, stream) : backward_f<KQ_F16, false>(g, groups, stream);
+    else
+        st = rag ? backward_f<KQ_F32, true>(g, groups, stream) : backward_f<KQ_F32, false>(g, groups, stream);
     if (st != KQ_OK || g.parts == 1 || (dweight == nullptr && dbias == nullptr)) return st;
-    const int64_t total = groups * 2 * d;
-    const int blocks = static_cast<int>(
-        std::min<int64_t>((total + 255) / 256, static_cast<int64_t>(info.sm_count) * 8));
-    return launch_pdl(norm_reduce_kernel, blocks, 256, 0, stream, g, groups);
+    const int64_t blocks = groups * ((2 * d + 31) / 32);
+    return launch_pdl(norm_reduce_kernel, static_cast<int>(blocks), 512, 0, stream, g);
 }
 
 }  // namespace kq
