@@ -111,6 +111,14 @@ typedef enum kq_format {
     KQ_F32 = 2
 } kq_format;
 
+/* Activations of the linear layers. */
+typedef enum kq_activation {
+    KQ_ACT_NONE = 0,
+    KQ_ACT_GELU = 1,        /* x (1 + erf(x / sqrt 2)) / 2 */
+    KQ_ACT_GELU_TANH = 2,   /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+    KQ_ACT_SILU = 3         /* x / (1 + exp(-x)) */
+} kq_activation;
+
 /* Alignment rules shared by the quantizer entry points:
  *   A, q, sf, y_debug, factors, s, K_expanded: 16-byte aligned;
  *   lda % 8 == 0 (16-byte row pitch), ldq % 16 == 0. */
@@ -348,6 +356,43 @@ KQ_API kq_status kq_layer_norm_backward(const void *dy, int64_t lddy, const void
 /* Workspace bytes of kq_layer_norm_backward (0 if none, or if the arguments
  * are invalid). */
 KQ_API size_t kq_layer_norm_backward_bytes(int64_t m, int64_t d, int64_t group_rows);
+
+/*
+ * kq_w4a4_linear -- a whole linear layer on the quantizer's output: the
+ * product of kq_w4a4_gemm with the layer's bias, activation and residual in
+ * its epilogue,
+ *     out = residual + act(deq(qa) deq(qw)^T + bias)
+ * on the fp32 accumulator, rounded once to out_fmt.  From one token (m = 1) up:
+ * calls with few output tiles split the contraction over clusters of CTAs.
+ *   qa, ldqa, sfa, qw, ldqw, sfw, m, n, k   as kq_w4a4_gemm (m, n, k <= 2^31,
+ *                    2^28, 2^28)
+ *   bias             device fp32 [n], or NULL
+ *   act              KQ_ACT_*
+ *   residual, ldr    device, [m][ldr] in out_fmt, or NULL.  It may be `out`
+ *                    itself (same pointer and pitch): every element is read
+ *                    before it is written
+ *   out, ldo         device, [m][ldo] in out_fmt (written, columns < n)
+ * Pointers are 16-byte aligned and the pitches of out and residual multiples
+ * of 16 bytes.  A pipeline that stalls for about a second stops as in
+ * kq_w4a4_gemm (tiles not written, or written as NaN).
+ */
+KQ_API kq_status kq_w4a4_linear(const uint8_t *qa, int64_t ldqa, const uint8_t *sfa,
+                                const uint8_t *qw, int64_t ldqw, const uint8_t *sfw, int64_t m,
+                                int64_t n, int64_t k, const float *bias, kq_activation act,
+                                const void *residual, int64_t ldr, void *out, int64_t ldo,
+                                kq_format out_fmt, cudaStream_t stream);
+
+/*
+ * kq_linear -- the unquantized layer, out = residual + act(a w^T + bias), for
+ * 16-bit operands.
+ *   a, lda, w, ldw   device, [m][lda] and [n][ldw] in in_fmt (KQ_BF16 or
+ *                    KQ_F16), lda, ldw >= k and % 8 == 0; any k >= 1
+ *   other arguments as kq_w4a4_linear
+ */
+KQ_API kq_status kq_linear(const void *a, int64_t lda, const void *w, int64_t ldw, kq_format in_fmt,
+                           int64_t m, int64_t n, int64_t k, const float *bias, kq_activation act,
+                           const void *residual, int64_t ldr, void *out, int64_t ldo,
+                           kq_format out_fmt, cudaStream_t stream);
 
 /*
  * kq_expand_blocks -- [KQ] Sec. 3.5.1 K1 (the dense 32x32 blocks are kept

@@ -1,5 +1,5 @@
 // C ABI entry points of the transformer-block operators around the quantizer
-// (layer norm): the argument checks, which run before anything is enqueued.
+// (layer norm, linear layer): the argument checks, which run before anything is enqueued.
 #include "kq_internal.h"
 
 using namespace kq;
@@ -8,6 +8,7 @@ namespace {
 
 constexpr int64_t kMaxRows = 0x7fffffffLL;       // grid and TMA coordinates are 32-bit
 constexpr int64_t kMaxPitch = 1LL << 38;
+constexpr int64_t kMaxCols = 1LL << 28;
 constexpr int64_t kMaxNorm = 16384;              // channels a team of threads holds in registers
 
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
@@ -23,6 +24,28 @@ bool norm_shape_ok(int64_t m, int64_t d, int64_t group_rows)
 int64_t norm_groups(int64_t m, int64_t group_rows)
 {
     return group_rows == 0 ? 1 : (m + group_rows - 1) / group_rows;
+}
+
+// The parts common to both linear layers: output, bias, activation, residual.
+kq_status check_linear(const LinearCall &c)
+{
+    if (c.fmt_out != KQ_BF16 && c.fmt_out != KQ_F16 && c.fmt_out != KQ_F32) return KQ_ERR_LAYOUT;
+    if (c.act < KQ_ACT_NONE || c.act > KQ_ACT_SILU) return KQ_ERR_LAYOUT;
+    // 32-bit TMA coordinates, in bytes across a row of the output
+    if (c.m < 0 || c.n < 0 || c.k <= 0 || c.m > kMaxRows || c.n > kMaxCols || c.k > kMaxCols ||
+        c.ldo < c.n || c.ldo > kMaxPitch || c.lda > kMaxPitch || c.ldw > kMaxPitch ||
+        (c.residual != nullptr && (c.ldr < c.n || c.ldr > kMaxPitch)))
+        return KQ_ERR_SHAPE;
+    if (c.m == 0 || c.n == 0) return KQ_OK;
+    if (c.a == nullptr || c.w == nullptr || c.out == nullptr) return KQ_ERR_NULL;
+    if (c.mx && (c.sfa == nullptr || c.sfw == nullptr)) return KQ_ERR_NULL;
+    const kq_format fmt = static_cast<kq_format>(c.fmt_out);
+    if (!aligned16(c.a) || !aligned16(c.w) || !aligned16(c.sfa) || !aligned16(c.sfw) ||
+        !aligned16(c.out) || !aligned16(c.bias) || !aligned16(c.residual) ||
+        c.lda % (c.mx ? 16 : 8) != 0 || c.ldw % (c.mx ? 16 : 8) != 0 || !pitch_ok(c.ldo, fmt) ||
+        (c.residual != nullptr && !pitch_ok(c.ldr, fmt)))
+        return KQ_ERR_ALIGN;
+    return KQ_OK;
 }
 
 }  // namespace
@@ -86,6 +109,34 @@ size_t kq_layer_norm_backward_bytes(int64_t m, int64_t d, int64_t group_rows)
     if (parts <= 1) return 0;
     return static_cast<size_t>(norm_groups(m, group_rows)) * static_cast<size_t>(parts) * 2u *
            static_cast<size_t>(d) * sizeof(float);
+}
+
+kq_status kq_w4a4_linear(const uint8_t *qa, int64_t ldqa, const uint8_t *sfa, const uint8_t *qw,
+                         int64_t ldqw, const uint8_t *sfw, int64_t m, int64_t n, int64_t k,
+                         const float *bias, kq_activation act, const void *residual, int64_t ldr,
+                         void *out, int64_t ldo, kq_format out_fmt, cudaStream_t stream)
+{
+    const LinearCall c = {true, qa, ldqa, sfa, qw, ldqw, sfw, KQ_BF16, m, n, k, bias,
+                          static_cast<int>(act), residual, ldr, out, ldo, static_cast<int>(out_fmt)};
+    if (k <= 0 || k % 32 != 0 || ldqa < k / 2 || ldqw < k / 2) return KQ_ERR_SHAPE;
+    const kq_status st = check_linear(c);
+    if (st != KQ_OK || m == 0 || n == 0) return st;
+    return launch_linear(c, stream);
+}
+
+kq_status kq_linear(const void *a, int64_t lda, const void *w, int64_t ldw, kq_format in_fmt,
+                    int64_t m, int64_t n, int64_t k, const float *bias, kq_activation act,
+                    const void *residual, int64_t ldr, void *out, int64_t ldo, kq_format out_fmt,
+                    cudaStream_t stream)
+{
+    if (in_fmt != KQ_BF16 && in_fmt != KQ_F16) return KQ_ERR_LAYOUT;
+    const LinearCall c = {false, a, lda, nullptr, w, ldw, nullptr, static_cast<int>(in_fmt), m, n, k,
+                          bias, static_cast<int>(act), residual, ldr, out, ldo,
+                          static_cast<int>(out_fmt)};
+    if (k <= 0 || lda < k || ldw < k) return KQ_ERR_SHAPE;
+    const kq_status st = check_linear(c);
+    if (st != KQ_OK || m == 0 || n == 0) return st;
+    return launch_linear(c, stream);
 }
 
 }  // extern "C"

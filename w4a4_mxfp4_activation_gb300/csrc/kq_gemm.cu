@@ -37,7 +37,9 @@
 #include <mutex>
 
 #include "kq_device.cuh"
+#include "kq_epilogue.cuh"
 #include "kq_internal.h"
+#include "kq_tcgen05.cuh"
 
 namespace kq {
 namespace {
@@ -55,28 +57,6 @@ constexpr int kGBarOff = kGRingOff + kGStages * kGStageBytes;
 constexpr int kGSmemBytes = kGBarOff + 1024 + 1024;
 constexpr uint32_t kGTmemCols = 256;
 
-__device__ __forceinline__ void g_tmem_alloc(uint32_t slot, uint32_t ncols)
-{
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(slot),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void g_tmem_dealloc(uint32_t taddr, uint32_t ncols)
-{
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void g_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void g_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-__device__ __forceinline__ uint64_t g_desc(uint32_t saddr)
-{
-    // K-major, 128B swizzle: LBO 16 B (unused), SBO 1024 B (8 rows x 128 B)
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16 >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-
 // kind::f16: fp32 D, bf16 A and B, both K-major, N = 128, M = 128.
 constexpr uint32_t kGIdesc = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) |
                              ((128u >> 4) << 24);
@@ -89,43 +69,6 @@ __device__ __forceinline__ void g_mma(uint32_t d, uint64_t a, uint64_t b, uint32
         "l"(a), "l"(b), "r"(kGIdesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void g_mma_id(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
-
-__device__ __forceinline__ void g_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void g_ld32(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
-{
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
-                 "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
 // E2M1 code (bits 0-2 magnitude, bit 3 sign) times 2^(byte - 127), as fp32:
 // exact (at most two significant bits; 2^-127 and below are fp32 subnormals).
 __device__ __forceinline__ float e2m1_scaled(uint32_t code, float scale)
@@ -146,6 +89,16 @@ __device__ __forceinline__ float e8m0_value(uint32_t byte)
     return __uint_as_float(byte == 255u ? 0x7FC00000u : (byte ? byte << 23 : 0x00400000u));
 }
 
+// The fused epilogue of the linear layers (see kq_epilogue.cuh).
+struct EpiArgs {
+    const float *bias;            // [n] or null
+    const void *residual;         // [m][ldr] in the output's type, or null
+    int64_t ldr;
+    void *out;                    // [m][ldo]
+    int64_t ldo;
+    int fmt, act;                 // kq_format, kq_activation
+};
+
 struct GemmArgs {
     int64_t m, n, k;              // C is m x n, the contraction runs over k
     int64_t nb;                   // k / 32 scale blocks per row
@@ -154,6 +107,8 @@ struct GemmArgs {
     float *c;
     int64_t ldc;
     int64_t mtiles, ntiles, ksteps;
+    int f16;                      // 16-bit operands are fp16 (linear layers), not bf16
+    EpiArgs epi;                  // linear layers only
 };
 
 __global__ void __launch_bounds__(kGThreads, 1)
@@ -390,17 +345,22 @@ constexpr int kXACodeBytes = 128 * 128;            // A codes per stage
 constexpr uint32_t kXTmemCols = 512;
 constexpr uint32_t kXSfCol = 256;                  // scale columns follow the accumulators
 
+// EPI: what the epilogue does with the accumulator: 0 stores it (the plain
+// products), 2 and 4 run the linear layers' epilogue with an output of that
+// many bytes an element.
 // MX = true: the FP4 product (codes + scale tiles, kind::mxf4, K = 256 per
 // stage); MX = false: the bf16 product A W^T on the same structure (kind::f16,
 // K = 64 per stage -- again 128 bytes of every operand row -- no scales).
-template <int NH, bool MX>
+template <int NH, bool MX, int EPI = 0>
 struct XCfg {
     static constexpr int kBN = 128 * NH;                  // tile width (C columns, W rows)
     static constexpr int kBK = MX ? 256 : 64;             // K elements per stage
     static constexpr int kStages = 4;
     static constexpr int kEpiWarps = 4 * NH;
     static constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer, MMA, epilogue
-    static constexpr int kAccBufs = NH == 1 ? 2 : 1;
+    // the bf16 product has no scales in TMEM, so a linear layer's wide tile has
+    // room for a second accumulator; the plain product releases its only one early
+    static constexpr int kAccBufs = NH == 1 || (EPI != 0 && !MX) ? 2 : 1;
     static constexpr int kWCodeBytes = kBN * 128;
     static constexpr int kSfaOff = kXACodeBytes + kWCodeBytes;
     static constexpr int kSfwOff = kSfaOff + 1024;        // A: two scale tiles; W: NH halves x 2
@@ -408,68 +368,159 @@ struct XCfg {
     // per epilogue warp kBoxBufs staging boxes of 32 rows x kBoxCols fp32 for
     // the TMA stores of C (128-byte swizzle for 32 columns, 64-byte for 16);
     // the wide tile keeps 4 stages by storing narrower boxes, one at a time
-    static constexpr int kBoxCols = NH == 1 ? 32 : 16;
-    static constexpr int kBoxBufs = NH == 1 ? 2 : 1;
-    static constexpr int kBoxBytes = 32 * kBoxCols * 4;
+    // (linear layers: boxes of 32 rows x 64 bytes)
+    static constexpr int kBoxCols = EPI != 0 ? 64 / EPI : (NH == 1 ? 32 : 16);
+    static constexpr int kBoxBufs = NH == 1 ? (EPI != 0 ? 4 : 2) : 1;
+    static constexpr int kBoxBytes = 32 * kBoxCols * (EPI != 0 ? EPI : 4);
     static constexpr int kStagingOff = kStages * kStageBytes;
     static constexpr int kBarOff = kStagingOff + kEpiWarps * kBoxBufs * kBoxBytes;
     static constexpr int kSmemBytes = kBarOff + 256 + 1024;
     static constexpr uint32_t kSfStride = 8 + 8 * NH;     // TMEM scale columns per stage
     static_assert(kStageBytes % 1024 == 0, "stages keep the 1 KB alignment of the swizzle");
-    static_assert(kXSfCol + kSfStride * kStages <= kXTmemCols, "scale columns fit in TMEM");
+    static_assert(!MX || kXSfCol + kSfStride * kStages <= kXTmemCols, "scale columns fit in TMEM");
+    static_assert(kAccBufs * kBN <= (MX ? 256 : 512), "accumulators fit in TMEM");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 };
 
-// Shared-memory descriptor of a no-swizzle K-major matrix: core matrices of
-// 8 rows x 16 bytes, SBO = distance between 8-row groups (one 16-byte chunk
-// per row here, so the chunk stride is unused).
-__device__ __forceinline__ uint64_t x_desc_noswz(uint32_t saddr, uint32_t sbo)
-{
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(16 >> 4) << 16) |
-           (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46);
-}
+// The linear layers' epilogue of one warp: 32 rows (one a lane) x 128 columns of
+// the tile, 64 bytes of output per row at a time.  The accumulator is read in
+// these steps and released after the last one: the loop is not unrolled, so
+// that three activations fit the instruction cache.  Each lane fetches its row's
+// residual one step ahead, and the first one before the accumulator is ready.
+// The boxes leave through TMA stores, which write whole 16-byte units: columns
+// past the last whole unit of a row are stored directly.
+template <int SIZE, int BUFS>
+struct LinearEpilogue {
+    static constexpr int kCols = 64 / SIZE;           // columns per step
+    static constexpr int kUnit = 16 / SIZE;           // columns per 16 bytes
 
-// Instruction descriptor of kind::mxf4: E2M1 A and B (format 1), both K-major,
-// UE8M0 scales (bit 23), N = 128, M = 128, dense K = 64; the scale-data ids
-// (bits 4-5 for B, 29-30 for A) pick the byte of the 32-bit TMEM scale word
-// the instruction starts at.
-__host__ __device__ constexpr uint32_t x_idesc(uint32_t sf_id)
-{
-    return (sf_id << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | (1u << 23) |
-           ((128u >> 4) << 24) | (sf_id << 29);
-}
+    // the residual of columns col .. col + kCols - 1 of row `row`
+    static __device__ __forceinline__ void fetch(const GemmArgs &g, int64_t row, int64_t col,
+                                                 uint4 (&r)[4])
+    {
+        const uint8_t *p = static_cast<const uint8_t *>(g.epi.residual);
+        if (p == nullptr || row >= g.m) return;
+        p += (row * g.epi.ldr + col) * SIZE;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (col + kUnit * (q + 1) <= g.n)
+                asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r[q].x), "=r"(r[q].y), "=r"(r[q].z), "=r"(r[q].w)
+                             : "l"(p + 16 * q)
+                             : "memory");
+        }
+    }
 
-__device__ __forceinline__ void x_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                      uint32_t sfa, uint32_t sfb, uint32_t acc)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
-        : "memory");
-}
+    // x0, y0: the first column and row of the warp's part; taddr: its
+    // accumulator; stg: its staging boxes; nbox: boxes written so far.
+    static __device__ __forceinline__ void run(const GemmArgs &g, const CUtensorMap *tmC, int64_t x0,
+                                               int64_t y0, uint32_t taddr, uint32_t stg,
+                                               int64_t &nbox, uint4 (&r)[4])
+    {
+        const int lane = threadIdx.x & 31;
+        const int64_t row = y0 + lane;
+        const int64_t whole = g.n & ~int64_t(kUnit - 1);   // columns the TMA store writes
+        const bool f16 = g.epi.fmt == KQ_F16;
+        const uint32_t sw = static_cast<uint32_t>((lane >> 1) & 3);   // 64-byte swizzle
+#pragma unroll 1
+        for (int c = 0; c < 128 / kCols; ++c) {
+            const int64_t col = x0 + kCols * c;
+            if (col >= g.n || y0 >= g.m) break;
+            uint32_t a[kCols];
+            if constexpr (SIZE == 2)
+                g_ld32(taddr + kCols * c, a);
+            else
+                g_ld16(taddr + kCols * c, a);
+            float v[kCols];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) v[j] = __uint_as_float(a[j]);
+            if (g.epi.bias != nullptr) {
+                if (col + kCols <= g.n) {
+#pragma unroll
+                    for (int j = 0; j < kCols; j += 4) {
+                        const float4 b = __ldg(reinterpret_cast<const float4 *>(g.epi.bias + col + j));
+                        v[j] += b.x;
+                        v[j + 1] += b.y;
+                        v[j + 2] += b.z;
+                        v[j + 3] += b.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j)
+                        if (col + j < g.n) v[j] += __ldg(g.epi.bias + col + j);
+                }
+            }
+            apply_act(v, g.epi.act);
+            if (g.epi.residual != nullptr) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (col + kUnit * (q + 1) <= g.n) {
+                        const uint32_t w[4] = {r[q].x, r[q].y, r[q].z, r[q].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (SIZE == 2) {
+                                const float2 f = unpack16(w[i], f16);
+                                v[kUnit * q + 2 * i] += f.x;
+                                v[kUnit * q + 2 * i + 1] += f.y;
+                            } else {
+                                v[kUnit * q + i] += __uint_as_float(w[i]);
+                            }
+                        }
+                    } else if (row < g.m) {
+#pragma unroll
+                        for (int i = 0; i < kUnit; ++i)
+                            if (col + kUnit * q + i < g.n)
+                                v[kUnit * q + i] += load_residual(
+                                    g.epi.residual, row * g.epi.ldr + col + kUnit * q + i, g.epi.fmt);
+                    }
+                }
+                if (col + kCols < x0 + 128) fetch(g, row, col + kCols, r);
+            }
+            if (col < whole) {
+                const uint32_t buf = stg + 2048u * static_cast<uint32_t>(nbox % BUFS);
+                if (nbox >= BUFS) {                       // the box's last store has read it
+                    if (lane == 0) bulk_wait_group_read<BUFS - 1>();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint4 o;
+                    if constexpr (SIZE == 2) {
+                        o = make_uint4(pack16(v[8 * q], v[8 * q + 1], f16),
+                                       pack16(v[8 * q + 2], v[8 * q + 3], f16),
+                                       pack16(v[8 * q + 4], v[8 * q + 5], f16),
+                                       pack16(v[8 * q + 6], v[8 * q + 7], f16));
+                    } else {
+                        o = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                       __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+                    }
+                    sts128(buf + static_cast<uint32_t>(64 * lane) + ((static_cast<uint32_t>(q) ^ sw) << 4), o);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(tmC, static_cast<int32_t>(col * SIZE), static_cast<int32_t>(y0), buf);
+                    bulk_commit_group();
+                }
+                __syncwarp();
+                ++nbox;
+            }
+            if (col + kCols > whole && row < g.m) {
+#pragma unroll
+                for (int j = 0; j < kCols; ++j)
+                    if (col + j >= whole && col + j < g.n)
+                        store_out(g.epi.out, row * g.epi.ldo + col + j, g.epi.fmt, v[j]);
+            }
+        }
+    }
+};
 
-// elect.sync: one lane of the converged warp.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t pred;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(pred));
-    return pred != 0;
-}
-
-__device__ __forceinline__ void x_cp_sf(uint32_t taddr, uint64_t sdesc)
-{
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-                 : "memory");
-}
-
-template <int NH, bool MX>
-__global__ void __launch_bounds__(XCfg<NH, MX>::kThreads, 1)
+template <int NH, bool MX, int EPI>
+__global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
     w4a4_mxf4_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmW,
                      const __grid_constant__ CUtensorMap tmC, const GemmArgs g)
 {
-    using C = XCfg<NH, MX>;
+    using C = XCfg<NH, MX, EPI>;
     constexpr int kXStages = C::kStages, kXBN = C::kBN, kXWCodeBytes = C::kWCodeBytes;
     constexpr int kXBK = C::kBK;
     constexpr int kXSfaOff = C::kSfaOff, kXSfwOff = C::kSfwOff, kXStageBytes = C::kStageBytes;
@@ -582,7 +633,7 @@ __global__ void __launch_bounds__(XCfg<NH, MX>::kThreads, 1)
             if (use >= 1)
                 ok = __all_sync(0xffffffffu,
                                 mbar_wait(acc_empty + 8 * b, static_cast<uint32_t>((use - 1) & 1)));
-            const uint32_t acc = tmem_base + 128 * b;
+            const uint32_t acc = tmem_base + static_cast<uint32_t>(kXBN * b);
             if (ok) ok = wait_full(kk);
             for (int64_t ks = 0; ks < g.ksteps && ok; ++ks, ++kk) {
                 const int s = static_cast<int>(kk % kXStages);
@@ -640,9 +691,11 @@ __global__ void __launch_bounds__(XCfg<NH, MX>::kThreads, 1)
                 } else {
                     if (leader && !MX) {
                         // kind::f16: four K = 16 steps of 32 bytes; zero fill past k
-                        constexpr uint32_t kIdF16 = (1u << 4) | (1u << 7) | (1u << 10) |
-                                                    ((static_cast<uint32_t>(kXBN) >> 3) << 17) |
-                                                    ((128u >> 4) << 24);
+                        constexpr uint32_t kIdBf16 = (1u << 4) | (1u << 7) | (1u << 10) |
+                                                     ((static_cast<uint32_t>(kXBN) >> 3) << 17) |
+                                                     ((128u >> 4) << 24);
+                        const uint32_t kIdF16 =
+                            EPI != 0 && g.f16 ? kIdBf16 & ~((1u << 7) | (1u << 10)) : kIdBf16;
                         for (int j = 0; j < 4; ++j)
                             g_mma_id(acc, da + 2 * j, db + 2 * j, kIdF16, (ks > 0 || j > 0) ? 1u : 0u);
                     }
@@ -682,10 +735,22 @@ __global__ void __launch_bounds__(XCfg<NH, MX>::kThreads, 1)
         int64_t tc = 0, nbox = 0;
         for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
             const int b = static_cast<int>(tc % C::kAccBufs);
+            uint4 resid[4];
+            const int64_t ey0 = t / g.ntiles * 128 + 32 * qtr, ex0 = t % g.ntiles * kXBN + 128 * h;
+            if constexpr (EPI != 0)
+                LinearEpilogue<EPI, C::kBoxBufs>::fetch(g, ey0 + lane, ex0, resid);
             const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full + 8 * b,
                                                               static_cast<uint32_t>((tc / C::kAccBufs) & 1)));
             if (!ok) break;
             g_fence_after();
+            if constexpr (EPI != 0) {
+                const uint32_t acc = tmem_base + (static_cast<uint32_t>(qtr * 32) << 16) +
+                                     static_cast<uint32_t>(kXBN * b + 128 * h);
+                LinearEpilogue<EPI, C::kBoxBufs>::run(g, &tmC, ex0, ey0, acc, stg, nbox, resid);
+                g_fence_before();
+                mbar_arrive(acc_empty + 8 * b);
+                continue;
+            }
             uint32_t v[128];
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(qtr * 32) << 16) + 128 * (b + h);
             asm volatile(
@@ -864,20 +929,17 @@ __global__ void __launch_bounds__(256) layer_error_kernel(const float *__restric
     }
 }
 
-template <int NH, bool MX>
+template <int NH, bool MX, int EPI = 0>
 kq_status launch_mxf4_t(const CUtensorMap &ma, const CUtensorMap &mw, const CUtensorMap &mc,
                         const GemmArgs &g, int sm_count, cudaStream_t stream)
 {
-    using C = XCfg<NH, MX>;
-    auto kern = w4a4_mxf4_kernel<NH, MX>;
-    static GSlot slot;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KQ_ERR_CUDA;
-    std::call_once(slot.once[dev], [&] {
-        slot.err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             C::kSmemBytes);
+    using C = XCfg<NH, MX, EPI>;
+    auto kern = w4a4_mxf4_kernel<NH, MX, EPI>;
+    static DeviceOnce once;
+    const kq_status st = once.run([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
     });
-    if (slot.err[dev] != cudaSuccess) return KQ_ERR_CUDA;
+    if (st != KQ_OK) return st;
     const int64_t tiles = g.mtiles * g.ntiles;
     const int grid = static_cast<int>(std::min<int64_t>(tiles, sm_count));
     return launch_pdl(kern, grid, C::kThreads, static_cast<size_t>(C::kSmemBytes), stream, ma, mw, mc,
@@ -911,7 +973,7 @@ kq_status launch_w4a4_mxf4(const uint8_t *qa, int64_t ldqa, const uint8_t *sfa, 
     st = make_tensor_map_2d_u8(&mw, const_cast<uint8_t *>(qw), n, k / 2, ldqw, 128,
                                static_cast<uint32_t>(bn), CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != KQ_OK) return st;
-    GemmArgs g;
+    GemmArgs g{};
     g.m = m;
     g.n = n;
     g.k = k;
@@ -968,7 +1030,7 @@ kq_status launch_w4a4_gemm(const uint8_t *qa, int64_t ldqa, const uint8_t *sfa, 
     st = make_tensor_map_2d_u8(&mw, const_cast<uint8_t *>(qw), n, k / 2, ldqw, 32, kGBN,
                                CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != KQ_OK) return st;
-    GemmArgs g;
+    GemmArgs g{};
     g.m = m;
     g.n = n;
     g.k = k;
@@ -1010,7 +1072,7 @@ kq_status launch_bf16_gemm(const uint16_t *a, int64_t lda, const uint16_t *w, in
     st = make_tensor_map_2d_f32(&mc, c, m, n4, ldc, box_cols, 32,
                                 box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
     if (st != KQ_OK) return st;
-    GemmArgs g;
+    GemmArgs g{};
     g.m = m;
     g.n = n;
     g.k = k;
@@ -1025,6 +1087,68 @@ kq_status launch_bf16_gemm(const uint16_t *a, int64_t lda, const uint16_t *w, in
     g.ksteps = ksteps;
     return wide ? launch_mxf4_t<2, false>(ma, mw, mc, g, info.sm_count, stream)
                 : launch_mxf4_t<1, false>(ma, mw, mc, g, info.sm_count, stream);
+}
+
+// The linear layer on the products' kernel.
+kq_status launch_linear_tiles(const LinearCall &q, cudaStream_t stream)
+{
+    const int64_t m = q.m, n = q.n, k = q.k;
+    const bool mx = q.mx;
+    DeviceInfo info;
+    kq_status st = device_info(info);
+    if (st != KQ_OK) return st;
+    const int64_t bk = mx ? 256 : 64, mtiles = (m + 127) / 128, ksteps = (k + bk - 1) / bk;
+    // the products' wave model; with a single accumulator (mx) the wide tile's
+    // epilogue is exposed whole
+    auto cost = [&](int64_t bn, double per_stage, double per_tile) {
+        const int64_t tiles = mtiles * ((n + bn - 1) / bn);
+        const int64_t waves = (tiles + info.sm_count - 1) / info.sm_count;
+        return static_cast<double>(waves) * (static_cast<double>(ksteps) * per_stage + per_tile);
+    };
+    const bool wide = cost(256, 1.35, mx ? 6.0 : 1.0) < cost(128, 1.0, 0.5);
+    const int bn = wide ? 256 : 128;
+    CUtensorMap ma, mw, mc;
+    if (mx) {
+        st = make_tensor_map_2d_u8(&ma, const_cast<void *>(q.a), m, k / 2, q.lda, 128, 128,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st == KQ_OK)
+            st = make_tensor_map_2d_u8(&mw, const_cast<void *>(q.w), n, k / 2, q.ldw, 128,
+                                       static_cast<uint32_t>(bn), CU_TENSOR_MAP_SWIZZLE_128B);
+    } else {
+        // 16-bit words either way: the copies do not look at them
+        st = make_tensor_map_2d_bf16(&ma, q.a, m, k, q.lda, 64, 128);
+        if (st == KQ_OK) st = make_tensor_map_2d_bf16(&mw, q.w, n, k, q.ldw, 64, static_cast<uint32_t>(bn));
+    }
+    if (st != KQ_OK) return st;
+    const int size = q.fmt_out == KQ_F32 ? 4 : 2, unit = 16 / size;
+    const int64_t whole = std::max<int64_t>(n & ~int64_t(unit - 1), unit);
+    st = make_tensor_map_2d_u8(&mc, q.out, m, whole * size, q.ldo * size, 64, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    if (st != KQ_OK) return st;
+    GemmArgs g{};
+    g.m = m;
+    g.n = n;
+    g.k = k;
+    g.nb = mx ? k / 32 : 0;
+    g.ncb = (g.nb + 3) / 4;
+    g.sfa = q.sfa;
+    g.sfw = q.sfw;
+    g.f16 = !mx && q.fmt_in == KQ_F16;
+    g.mtiles = mtiles;
+    g.ntiles = (n + bn - 1) / bn;
+    g.ksteps = ksteps;
+    g.epi = {q.bias, q.residual, q.ldr, q.out, q.ldo, q.fmt_out, q.act};
+    if (mx) {
+        if (size == 2)
+            return wide ? launch_mxf4_t<2, true, 2>(ma, mw, mc, g, info.sm_count, stream)
+                        : launch_mxf4_t<1, true, 2>(ma, mw, mc, g, info.sm_count, stream);
+        return wide ? launch_mxf4_t<2, true, 4>(ma, mw, mc, g, info.sm_count, stream)
+                    : launch_mxf4_t<1, true, 4>(ma, mw, mc, g, info.sm_count, stream);
+    }
+    if (size == 2)
+        return wide ? launch_mxf4_t<2, false, 2>(ma, mw, mc, g, info.sm_count, stream)
+                    : launch_mxf4_t<1, false, 2>(ma, mw, mc, g, info.sm_count, stream);
+    return wide ? launch_mxf4_t<2, false, 4>(ma, mw, mc, g, info.sm_count, stream)
+                : launch_mxf4_t<1, false, 4>(ma, mw, mc, g, info.sm_count, stream);
 }
 
 }  // namespace kq

@@ -140,6 +140,30 @@ kq_status launch_norm_backward(const void *dy, int64_t lddy, const void *x, int6
                                int64_t lddx, float *dweight, float *dbias, void *workspace,
                                cudaStream_t stream);
 
+// A linear layer, out = residual + act(A W^T + bias).  mx: a and w are packed
+// MXFP4 codes (pitches in bytes) with their tiled scales, else 16-bit rows in
+// fmt_in (pitches in elements); residual and out are in fmt_out.
+struct LinearCall {
+    bool mx;
+    const void *a;
+    int64_t lda;
+    const uint8_t *sfa;
+    const void *w;
+    int64_t ldw;
+    const uint8_t *sfw;
+    int fmt_in;
+    int64_t m, n, k;
+    const float *bias;
+    int act;
+    const void *residual;
+    int64_t ldr;
+    void *out;
+    int64_t ldo;
+    int fmt_out;
+};
+kq_status launch_linear(const LinearCall &c, cudaStream_t stream);
+kq_status launch_linear_tiles(const LinearCall &c, cudaStream_t stream);   // the products' kernel
+
 kq_status validate_quant_args(const uint16_t *A, int64_t m, int64_t d, int64_t lda,
                               const uint8_t *q, int64_t ldq, const uint8_t *sf,
                               kq_sf_layout layout, const float *y_debug);

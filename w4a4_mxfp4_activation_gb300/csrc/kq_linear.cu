@@ -1,0 +1,359 @@
+// The linear layer out = residual + act(A W^T + bias) on the tensor cores,
+// sm_103a: the choice of kernel, and the kernel for calls with few output tiles.
+//
+// Calls whose 128 x 128 output tiles fill the SMs run on the products' kernel
+// (kq_gemm.cu) with the fused epilogue.  The others -- one token, a short
+// prompt -- are bound by the bytes of W and by latency: a 1 x 3072 x 12288 MXFP4
+// layer reads 20 MB of weights, 3 us of HBM time, from 24 tiles of 128 weight
+// rows.  split_kernel therefore splits the contraction of a tile over a cluster
+// of up to 8 CTAs, so that most SMs stream weights, and joins the parts through
+// distributed shared memory: no workspace, no second launch, and a fixed order
+// of the additions.  The weight rows are the M side of its MMAs (128 rows, one
+// TMEM lane each) and the tokens the N side (16 to 128), so a token costs one
+// accumulator column and not one of 128 padded rows.
+#include <algorithm>
+
+#include "kq_device.cuh"
+#include "kq_epilogue.cuh"
+#include "kq_internal.h"
+#include "kq_tcgen05.cuh"
+
+namespace kq {
+namespace {
+
+constexpr int kSWBytes = 128 * 128;                 // W per stage: 128 rows x 128 bytes
+constexpr int kSThreads = 192;                      // producer, MMA, 4 epilogue warps
+constexpr int kSMaxStages = 8;
+constexpr int kSBarBytes = 256;
+constexpr int kSRingBytes = 200 * 1024;
+constexpr uint32_t kSTmemCols = 256;                // accumulator <= 128, scales 16 a stage
+constexpr uint32_t kSSfCol = 128;
+constexpr int kSMaxSplit = 8;                       // portable cluster size
+
+struct SplitArgs {
+    int64_t m, n, k;
+    int64_t nb, ncb;              // MXFP4: k / 32 blocks, ceil(nb / 4) scale tiles
+    const uint8_t *sfa, *sfw;
+    int64_t ntiles;               // tiles of 128 weight rows
+    int ksteps;                   // K stages (256 MXFP4 or 64 16-bit elements)
+    int tokens;                   // tokens per tile, a multiple of 16
+    int stages, splits;
+    int f16;                      // 16-bit operands are fp16
+    const float *bias;
+    const void *residual;
+    int64_t ldr;
+    void *out;
+    int64_t ldo;
+    int fmt, act;
+};
+
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16 bytes of another CTA's shared memory at this CTA's address `addr`.
+__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank)
+{
+    uint32_t p;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(p) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(p)
+                 : "memory");
+    return v;
+}
+
+template <bool MX>
+__global__ void __launch_bounds__(kSThreads, 1)
+    split_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                 const SplitArgs g)
+{
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bar = base + kSRingBytes;
+    const uint32_t full = bar, empty = bar + 8 * kSMaxStages, done = bar + 16 * kSMaxStages;
+    const uint32_t tmem_slot = done + 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(blockIdx.x % static_cast<unsigned>(g.splits));
+    const int64_t tile = blockIdx.x / static_cast<unsigned>(g.splits);
+    const int64_t nt = tile % g.ntiles, mt = tile / g.ntiles;
+    const int k0 = static_cast<int>(static_cast<int64_t>(g.ksteps) * rank / g.splits);
+    const int k1 = static_cast<int>(static_cast<int64_t>(g.ksteps) * (rank + 1) / g.splits);
+    const uint32_t xbytes = static_cast<uint32_t>(g.tokens) * 128u;
+    const uint32_t sfw_off = kSWBytes + xbytes, sfx_off = sfw_off + 1024u;
+    const uint32_t stage_bytes = sfw_off + (MX ? 2048u : 0u);
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        for (int s = 0; s < g.stages; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        mbar_init(done, 1);
+        mbar_fence_init();
+    }
+    if (warp == 1) g_tmem_alloc(tmem_slot, kSTmemCols);
+    g_fence_before();
+    __syncthreads();
+    g_fence_after();
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+    grid_dependency_wait();
+
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int s = 0, issued = 0;
+            uint32_t par = 1;                        // the first round needs no wait
+            for (int ks = k0; ks < k1; ++ks) {
+                if (ks - k0 >= g.stages && !mbar_wait(empty + 8 * s, par)) break;
+                const uint32_t st = base + static_cast<uint32_t>(s) * stage_bytes, fb = full + 8 * s;
+                uint32_t sf_bytes = 0;
+                if constexpr (MX) {
+                    // scale tiles (4 blocks wide) of this stage's instructions
+                    const int64_t rem = (g.k - static_cast<int64_t>(ks) * 256 + 63) / 64;
+                    sf_bytes = static_cast<uint32_t>((min(rem, int64_t(4)) + 1) / 2) * 512u;
+                }
+                mbar_arrive_expect_tx(fb, kSWBytes + xbytes + 2 * sf_bytes);
+                const int32_t x = ks * (MX ? 128 : 64);
+                tma_load_2d(st, &tmW, x, static_cast<int32_t>(nt * 128), fb, 0);
+                tma_load_2d(st + kSWBytes, &tmX, x, static_cast<int32_t>(mt * g.tokens), fb, 0);
+                if constexpr (MX) {
+                    bulk_load(st + sfw_off, g.sfw + (nt * g.ncb + 2 * ks) * 512, sf_bytes, fb);
+                    bulk_load(st + sfx_off, g.sfa + (mt * g.ncb + 2 * ks) * 512, sf_bytes, fb);
+                }
+                ++issued;
+                if (++s == g.stages) {
+                    s = 0;
+                    par ^= 1;
+                }
+            }
+            // the last copies have landed before the ring is reused or left
+            for (int j = max(0, issued - g.stages); j < issued; ++j)
+                (void)mbar_wait(full + 8 * (j % g.stages), static_cast<uint32_t>((j / g.stages) & 1));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const bool leader = elect_one();
+        const bool pad_fix = MX && (g.nb & 1) != 0;
+        const uint32_t nbits = static_cast<uint32_t>(g.tokens >> 3) << 17;
+        const uint32_t idx = (x_idesc(0) & ~(63u << 17)) | nbits;
+        uint32_t idf = (1u << 4) | (1u << 7) | (1u << 10) | nbits | ((128u >> 4) << 24);
+        if (g.f16) idf &= ~((1u << 7) | (1u << 10));
+        int s = 0;
+        uint32_t par = 0;
+        for (int ks = k0; ks < k1 && ok; ++ks) {
+            ok = __all_sync(0xffffffffu, mbar_wait(full + 8 * s, par));
+            if (!ok) break;
+            const uint32_t st = base + static_cast<uint32_t>(s) * stage_bytes;
+            int nmma = 4;
+            if constexpr (MX) {
+                nmma = static_cast<int>(min((g.k - static_cast<int64_t>(ks) * 256 + 63) / 64, int64_t(4)));
+                if (pad_fix && ks == g.ksteps - 1) {
+                    // the padding block of an odd block count: scale 2^0, so that a
+                    // NaN byte there cannot meet the zero codes
+                    const int kb = static_cast<int>(g.nb - 8 * static_cast<int64_t>(ks));
+                    const uint32_t off = static_cast<uint32_t>((kb >> 2) * 512 + 16 * lane + (kb & 3));
+#pragma unroll
+                    for (int grp = 0; grp < 4; ++grp) {
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(st + sfw_off + off + 4 * grp), "r"(127u) : "memory");
+                        asm volatile("st.shared.u8 [%0], %1;" ::"r"(st + sfx_off + off + 4 * grp), "r"(127u) : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+            g_fence_after();
+            if (leader) {
+                const uint64_t dw = g_desc(st), dx = g_desc(st + kSWBytes);
+                const uint32_t first = ks > k0 ? 1u : 0u;
+                if constexpr (MX) {
+                    const uint32_t sft = tmem + kSSfCol + 16u * static_cast<uint32_t>(s);
+                    const uint64_t dsw = x_desc_noswz(st + sfw_off, 128), dsx = x_desc_noswz(st + sfx_off, 128);
+                    for (int at = 0; at < (nmma + 1) / 2; ++at) {
+                        x_cp_sf(sft + 4 * at, dsw + 32 * at);
+                        x_cp_sf(sft + 8 + 4 * at, dsx + 32 * at);
+                    }
+                    for (int j = 0; j < nmma; ++j) {
+                        // the scale-data id picks the block pair of the K = 64 step
+                        const uint32_t id = (j & 1) ? idx | (2u << 4) | (2u << 29) : idx;
+                        x_mma(tmem, dw + 2 * j, dx + 2 * j, id, sft + 4 * (j >> 1),
+                              sft + 8 + 4 * (j >> 1), first | (j > 0));
+                    }
+                } else {
+                    for (int j = 0; j < 4; ++j) g_mma_id(tmem, dw + 2 * j, dx + 2 * j, idf, first | (j > 0));
+                }
+                g_commit(empty + 8 * s);
+                if (ks == k1 - 1) g_commit(done);
+            }
+            __syncwarp();
+            if (++s == g.stages) {
+                s = 0;
+                par ^= 1;
+            }
+        }
+    }
+    // all warps: the accumulator is complete, and the ring free for the parts
+    ok = mbar_wait(done, 0, 2 * kWaitLimitNs) && ok;
+    __syncthreads();                                 // the producer's copies have landed too
+    const int rows = static_cast<int>(min(int64_t(g.tokens), g.m - mt * g.tokens));
+    if (warp >= 2) {
+        // part[token][weight row] in fp32; a part that is not there is NaN
+        const int q = warp & 3;
+        g_fence_after();
+        for (int c = 0; c < rows; c += 16) {
+            uint32_t a[16];
+            g_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + c, a);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + j) * 128 + q * 32 + lane) * 4),
+                             "r"(ok ? a[j] : 0x7FC00000u)
+                             : "memory");
+        }
+        g_fence_before();
+    }
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    // the tile's elements, four neighbouring channels a thread, spread over the
+    // cluster; every sum runs over the ranks in order
+    const int units = rows * 32;
+    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / g.splits);
+    const bool f16 = g.fmt == KQ_F16;
+    for (int u = static_cast<int>(static_cast<int64_t>(units) * rank / g.splits) + threadIdx.x; u < u1;
+         u += kSThreads) {
+        const int64_t row = mt * g.tokens + (u >> 5), col = nt * 128 + 4 * (u & 31);
+        if (col >= g.n) continue;
+        const uint32_t at = base + static_cast<uint32_t>(u) * 16u;
+        float4 p[kSMaxSplit];
+#pragma unroll
+        for (int r = 0; r < kSMaxSplit; ++r)
+            if (r < g.splits) p[r] = ld_peer(at, static_cast<uint32_t>(r));
+        float v[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
+#pragma unroll
+        for (int r = 1; r < kSMaxSplit; ++r) {
+            if (r < g.splits) {
+                v[0] += p[r].x;
+                v[1] += p[r].y;
+                v[2] += p[r].z;
+                v[3] += p[r].w;
+            }
+        }
+        const int left = static_cast<int>(min(int64_t(4), g.n - col));
+        if (g.bias != nullptr)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left) v[j] += __ldg(g.bias + col + j);
+        apply_act(v, g.act);
+        if (g.residual != nullptr)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left) v[j] += load_residual(g.residual, row * g.ldr + col + j, g.fmt);
+        const int64_t o = row * g.ldo + col;
+        if (left == 4 && g.fmt != KQ_F32) {
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.out) + o) =
+                make_uint2(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16));
+        } else if (left == 4) {
+            stg_f4(static_cast<float *>(g.out) + o, make_float4(v[0], v[1], v[2], v[3]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < left) store_out(g.out, o + j, g.fmt, v[j]);
+        }
+    }
+    __syncwarp();
+    cluster_arrive();                                // the parts have been read
+    cluster_wait();
+    if (warp == 1) {
+        g_fence_after();
+        g_tmem_dealloc(tmem, kSTmemCols);
+    }
+}
+
+template <bool MX>
+kq_status launch_split(const CUtensorMap &mx, const CUtensorMap &mw, const SplitArgs &g,
+                       int64_t tiles, cudaStream_t stream)
+{
+    constexpr int kSmem = kSRingBytes + kSBarBytes + 1024;
+    auto kern = split_kernel<MX>;
+    static DeviceOnce once;
+    const kq_status st = once.run([&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    });
+    if (st != KQ_OK) return st;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.splits));
+    cfg.blockDim = dim3(kSThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(g.splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, mx, mw, g) == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+}
+
+}  // namespace
+
+kq_status launch_linear(const LinearCall &c, cudaStream_t stream)
+{
+    DeviceInfo info;
+    kq_status st = device_info(info);
+    if (st != KQ_OK) return st;
+    const int64_t ntiles = (c.n + 127) / 128, mtiles = (c.m + 127) / 128, tiles = mtiles * ntiles;
+    const int64_t ksteps = (c.k + (c.mx ? 255 : 63)) / (c.mx ? 256 : 64);
+    const int64_t splits = std::min<int64_t>({kSMaxSplit, info.sm_count / tiles, ksteps});
+    if (splits < 2) return launch_linear_tiles(c, stream);
+
+    SplitArgs g{};
+    g.m = c.m;
+    g.n = c.n;
+    g.k = c.k;
+    g.nb = c.mx ? c.k / 32 : 0;
+    g.ncb = (g.nb + 3) / 4;
+    g.sfa = c.sfa;
+    g.sfw = c.sfw;
+    g.ntiles = ntiles;
+    g.ksteps = static_cast<int>(ksteps);
+    g.tokens = c.m >= 128 ? 128 : static_cast<int>((c.m + 15) / 16 * 16);
+    g.splits = static_cast<int>(splits);
+    const int stage = kSWBytes + g.tokens * 128 + (c.mx ? 2048 : 0);
+    g.stages = std::min(kSMaxStages, kSRingBytes / stage);
+    g.f16 = !c.mx && c.fmt_in == KQ_F16;
+    g.bias = c.bias;
+    g.residual = c.residual;
+    g.ldr = c.ldr;
+    g.out = c.out;
+    g.ldo = c.ldo;
+    g.fmt = c.fmt_out;
+    g.act = c.act;
+    CUtensorMap mx, mw;
+    const uint32_t rows = static_cast<uint32_t>(g.tokens);
+    if (c.mx) {
+        st = make_tensor_map_2d_u8(&mx, const_cast<void *>(c.a), c.m, c.k / 2, c.lda, 128, rows,
+                                   CU_TENSOR_MAP_SWIZZLE_128B);
+        if (st == KQ_OK)
+            st = make_tensor_map_2d_u8(&mw, const_cast<void *>(c.w), c.n, c.k / 2, c.ldw, 128, 128,
+                                       CU_TENSOR_MAP_SWIZZLE_128B);
+    } else {
+        st = make_tensor_map_2d_bf16(&mx, c.a, c.m, c.k, c.lda, 64, rows);
+        if (st == KQ_OK) st = make_tensor_map_2d_bf16(&mw, c.w, c.n, c.k, c.ldw, 64, 128);
+    }
+    if (st != KQ_OK) return st;
+    return c.mx ? launch_split<true>(mx, mw, g, tiles, stream)
+                : launch_split<false>(mx, mw, g, tiles, stream);
+}
+
+}  // namespace kq

@@ -26,6 +26,7 @@ KQ_K_FP32 = 0
 KQ_K_BF16X3 = 1
 KQ_IN_BF16 = 0
 KQ_IN_F16 = 1
+KQ_ACT = {"none": 0, "gelu": 1, "gelu_tanh": 2, "silu": 3}
 KQ_TRANSFORM = {"kron": 0, "diag": 1, "hadamard": 2, "identity": 3, "fwht": 4}
 VARIANT_BUTTERFLY = 0
 VARIANT_IDENTITY = 2
@@ -41,6 +42,7 @@ EXPORTS = (
     "kq_fwht_quantize_mxfp4", "kq_w4a4_gemm", "kq_bf16_gemm",
     "kq_layer_error", "kq_quantize_mxfp4_shared", "kq_quantize_mxfp4_ex",
     "kq_layer_norm", "kq_layer_norm_backward", "kq_layer_norm_backward_bytes",
+    "kq_w4a4_linear", "kq_linear",
 )
 TESTING_EXPORTS = (
     "kq_quantize_mxfp4_variant", "kq_w4a4_gemm_variant", "kq_test_encode_e2m1",
@@ -126,6 +128,12 @@ def lib() -> ctypes.CDLL:
             L.kq_layer_norm_backward.restype = st
             L.kq_layer_norm_backward_bytes.argtypes = [i64, i64, i64]
             L.kq_layer_norm_backward_bytes.restype = ctypes.c_size_t
+            L.kq_w4a4_linear.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, st, vp, i64, vp,
+                                         i64, st, vp]
+            L.kq_w4a4_linear.restype = st
+            L.kq_linear.argtypes = [vp, i64, vp, i64, st, i64, i64, i64, vp, st, vp, i64, vp, i64, st,
+                                    vp]
+            L.kq_linear.restype = st
             _lib = L
     return _lib
 
@@ -539,3 +547,51 @@ def kq_layer_norm_backward(dy, x, weight, mean, rstd, group_rows: int = 0, dx=No
                                         _stream(stream)),
            "kq_layer_norm_backward")
     return dx, dweight, dbias
+
+
+def _linear_out(m, n, residual, out, out_dtype, device):
+    """(out, residual pointer, residual pitch) of a linear layer."""
+    if out is None:
+        out = _empty_rows(m, n, out_dtype, device)
+    elif tuple(out.shape) != (m, n) or out.dtype != out_dtype:
+        raise ValueError(f"out must be [{m}, {n}] of {out_dtype}")
+    if residual is None:
+        return out, None, 0
+    if tuple(residual.shape) != (m, n) or residual.dtype != out_dtype:
+        raise ValueError(f"residual must be [{m}, {n}] of {out_dtype}")
+    return out, residual.data_ptr(), _rows(residual, "residual")
+
+
+def kq_w4a4_linear(qa, sfa, qw, sfw, m: int, n: int, k: int, bias=None, act: str = "none",
+                   residual=None, out=None, out_dtype=None, stream=None):
+    """residual + act(deq(qa) deq(qw)^T + bias) as [m, n] of ``out_dtype``
+    (bfloat16 when not given), from packed codes and 128x4 tiled scales.
+    bias: fp32 [n]; act in KQ_ACT; residual: [m, n] of ``out_dtype``."""
+    if out_dtype is None:
+        import torch
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    out, res, ldr = _linear_out(m, n, residual, out, out_dtype, qa.device)
+    _check(lib().kq_w4a4_linear(_ptr(qa), _ld(qa, k // 2), _ptr(sfa), _ptr(qw), _ld(qw, k // 2),
+                                _ptr(sfw), m, n, k, _f32(bias, "bias", n), KQ_ACT[act], res, ldr,
+                                _ptr(out), _rows(out, "out"), _format(out_dtype), _stream(stream)),
+           "kq_w4a4_linear")
+    return out
+
+
+def kq_linear(a, w, bias=None, act: str = "none", residual=None, out=None, out_dtype=None,
+              stream=None):
+    """residual + act(a w^T + bias) for a [m, k] and w [n, k], both bfloat16 or
+    both float16; the result is [m, n] of ``out_dtype`` (a's type when not
+    given).  bias: fp32 [n]; act in KQ_ACT; residual: [m, n] of ``out_dtype``."""
+    m, k = a.shape
+    n = w.shape[0]
+    if w.shape[1] != k or w.dtype != a.dtype:
+        raise ValueError("a and w must have the same number of columns and the same type")
+    if out_dtype is None:
+        out_dtype = a.dtype if out is None else out.dtype
+    out, res, ldr = _linear_out(m, n, residual, out, out_dtype, a.device)
+    _check(lib().kq_linear(_ptr(a), _rows(a, "a"), _ptr(w), _rows(w, "w"), _format(a.dtype), m, n, k,
+                           _f32(bias, "bias", n), KQ_ACT[act], res, ldr, _ptr(out),
+                           _rows(out, "out"), _format(out_dtype), _stream(stream)),
+           "kq_linear")
+    return out
