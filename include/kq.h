@@ -395,6 +395,53 @@ KQ_API kq_status kq_linear(const void *a, int64_t lda, const void *w, int64_t ld
                            kq_format out_fmt, cudaStream_t stream);
 
 /*
+ * kq_attention -- attention over a batch of packed sequences of different
+ * lengths, with groups of query heads sharing a key/value head:
+ *     out[i][h] = sum_j softmax_j(scale q[i][h] . k[j][h']) v[j][h']
+ *     lse[i][h] = log sum_j exp(scale q[i][h] . k[j][h'])
+ * with h' = h / (heads / kv_heads) and j over the keys of row i's sequence.
+ * From a whole prompt (as many queries as keys) to one new token against a long
+ * cache (one query): with `causal`, query row a of a sequence of qlen queries
+ * and klen keys sees keys 0 .. a + klen - qlen.  A row that sees no key gives
+ * out = 0, lse = -inf.  Scores, softmax and sums are fp32; the softmax weights
+ * are rounded to fmt for the product with v.
+ *   q, k, v          device, fmt (KQ_BF16 or KQ_F16); row (token t, head h) at
+ *                    t * X_token + h * X_head elements, d values each (strides
+ *                    >= d and multiples of 8: [token][head][d], head-major, or
+ *                    views of a packed QKV tensor)
+ *   cu_q, cu_k       device int32 [nseq + 1]: sequence b has query rows
+ *                    cu_q[b] .. cu_q[b + 1] - 1 and keys cu_k[b] ..; lengths of
+ *                    zero are allowed.  Offsets out of [0, tq] or [0, tk] are
+ *                    clamped to it; rows of no sequence are not written
+ *   tq, tk           rows of q and out, of k and v (< 2^31 - 1024)
+ *   heads, kv_heads  heads % kv_heads == 0, heads <= 65536
+ *   d                8 <= d <= 128, d % 8 == 0
+ *   max_q            an upper bound of the query lengths.  It chooses the
+ *                    schedule: too small a value costs speed, not correctness
+ *   causal           0 or 1
+ *   scale            > 0, finite (usually 1 / sqrt(d))
+ *   out              device, fmt, strides as q's (written; not q, k or v)
+ *   lse              device fp32 [tq][heads], or NULL
+ *   workspace        device, kq_attention_bytes() bytes, 16-byte aligned; NULL
+ *                    when that is 0.  It is only used during the call
+ * Pointers are 16-byte aligned.  A NaN or infinity in k or v of one sequence
+ * does not reach another.  Within a sequence a masked key has weight zero, and
+ * zero times a non-finite v is NaN for the rows of the same tile, as in the
+ * formula read literally.  The same inputs give the same bits.
+ */
+KQ_API kq_status kq_attention(const void *q, int64_t q_token, int64_t q_head, const void *k,
+                              int64_t k_token, int64_t k_head, const void *v, int64_t v_token,
+                              int64_t v_head, kq_format fmt, const int32_t *cu_q, const int32_t *cu_k,
+                              int64_t nseq, int64_t tq, int64_t tk, int64_t heads, int64_t kv_heads,
+                              int64_t d, int64_t max_q, int causal, float scale, void *out,
+                              int64_t out_token, int64_t out_head, float *lse, void *workspace,
+                              cudaStream_t stream);
+
+/* Workspace bytes of kq_attention (0 if none, or if the arguments are invalid). */
+KQ_API size_t kq_attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d,
+                                 int64_t max_q);
+
+/*
  * kq_expand_blocks -- [KQ] Sec. 3.5.1 K1 (the dense 32x32 blocks are kept
  * in device memory): expand the raw factors into dense blocks by eq. (12),
  * computed in fp64 and then rounded to the requested format.

@@ -58,6 +58,11 @@ kq_status make_tensor_map_2d_u8(CUtensorMap *map, void *base, int64_t rows, int6
 kq_status make_tensor_map_2d_f32(CUtensorMap *map, void *base, int64_t rows, int64_t cols,
                                  int64_t ld_elems, uint32_t box_cols, uint32_t box_rows,
                                  CUtensorMapSwizzle swizzle);
+// [d2][d1][d0] 16-bit elements (strides of d1 and d2 in elements), boxes with
+// rows of 128 bytes in the 128-byte swizzle.
+kq_status make_tensor_map_3d_16(CUtensorMap *map, const void *base, int64_t d0, int64_t d1, int64_t d2,
+                                int64_t stride1, int64_t stride2, uint32_t box0, uint32_t box1,
+                                uint32_t box2);
 kq_status check_launch();
 
 // Runs a kernel's one-time setup (cudaFuncSetAttribute) once per device.
@@ -163,6 +168,24 @@ struct LinearCall {
 };
 kq_status launch_linear(const LinearCall &c, cudaStream_t stream);
 kq_status launch_linear_tiles(const LinearCall &c, cudaStream_t stream);   // the products' kernel
+
+// Attention over packed sequences; strides in elements.  attention_bytes: its
+// workspace (0 where no item is split).
+struct AttentionCall {
+    const void *q, *k, *v;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+    bool f16;
+    const int32_t *cu_q, *cu_k;
+    int64_t nseq, tq, tk, heads, kv_heads, d, max_q;
+    bool causal;
+    float scale;
+    void *out;
+    int64_t out_token, out_head;
+    float *lse;
+    void *workspace;
+};
+size_t attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_q);
+kq_status launch_attention(const AttentionCall &c, cudaStream_t stream);
 
 kq_status validate_quant_args(const uint16_t *A, int64_t m, int64_t d, int64_t lda,
                               const uint8_t *q, int64_t ldq, const uint8_t *sf,

@@ -42,7 +42,7 @@ EXPORTS = (
     "kq_fwht_quantize_mxfp4", "kq_w4a4_gemm", "kq_bf16_gemm",
     "kq_layer_error", "kq_quantize_mxfp4_shared", "kq_quantize_mxfp4_ex",
     "kq_layer_norm", "kq_layer_norm_backward", "kq_layer_norm_backward_bytes",
-    "kq_w4a4_linear", "kq_linear",
+    "kq_w4a4_linear", "kq_linear", "kq_attention", "kq_attention_bytes",
 )
 TESTING_EXPORTS = (
     "kq_quantize_mxfp4_variant", "kq_w4a4_gemm_variant", "kq_test_encode_e2m1",
@@ -134,6 +134,11 @@ def lib() -> ctypes.CDLL:
             L.kq_linear.argtypes = [vp, i64, vp, i64, st, i64, i64, i64, vp, st, vp, i64, vp, i64, st,
                                     vp]
             L.kq_linear.restype = st
+            L.kq_attention.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, st, vp, vp, i64, i64,
+                                       i64, i64, i64, i64, i64, st, f32, vp, i64, i64, vp, vp, vp]
+            L.kq_attention.restype = st
+            L.kq_attention_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
+            L.kq_attention_bytes.restype = ctypes.c_size_t
             _lib = L
     return _lib
 
@@ -595,3 +600,58 @@ def kq_linear(a, w, bias=None, act: str = "none", residual=None, out=None, out_d
                            _rows(out, "out"), _format(out_dtype), _stream(stream)),
            "kq_linear")
     return out
+
+
+def _heads(t, what: str):
+    """(token stride, head stride) of a [tokens, heads, d] tensor."""
+    if t.dim() != 3:
+        raise ValueError(f"{what} must be [tokens, heads, d]")
+    n, h, d = t.shape
+    st, sh, s1 = t.stride()
+    if s1 != 1 and d > 1:
+        raise ValueError(f"{what}: the channels of a head must be adjacent in memory")
+    # strides of dimensions of one row or none are not used
+    sh = sh if h > 1 else d
+    return (st if n > 1 else max(h * sh, d)), sh
+
+
+def _offsets(t, what: str):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise TypeError(f"{what} must be a contiguous one-dimensional int32 tensor")
+    return t.numel() - 1
+
+
+def kq_attention(q, k, v, cu_q, cu_k, max_q: int, max_k: int | None = None, causal: bool = True,
+                 scale: float | None = None, lse: bool = False, out=None, stream=None):
+    """Attention over packed sequences: q [tq, heads, d], k and v [tk, kv_heads,
+    d] (bfloat16 or float16, any strides that are multiples of 8 elements),
+    sequence b in rows cu_q[b]..cu_q[b + 1] of q and cu_k[b]..cu_k[b + 1] of k and
+    v (int32 [nseq + 1]).  max_q bounds the query lengths (``max_k`` is not
+    needed); scale defaults to 1 / sqrt(d).  Returns out [tq, heads, d], or (out,
+    lse [tq, heads] fp32) with ``lse=True``."""
+    import torch
+    tq, heads, d = q.shape
+    tk, kv_heads = k.shape[0], k.shape[1]
+    if k.shape != v.shape or k.shape[2] != d or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("k and v must have one shape, and the type and last dimension of q")
+    nseq = _offsets(cu_q, "cu_q")
+    if _offsets(cu_k, "cu_k") != nseq:
+        raise ValueError("cu_q and cu_k must have the same number of entries")
+    if nseq < 0:
+        raise ValueError("cu_q and cu_k must have at least one entry")
+    if out is None:
+        out = torch.empty((tq, heads, d), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have the shape and type of q")
+    stats = torch.empty((tq, heads), dtype=torch.float32, device=q.device) if lse else None
+    L = lib()
+    nbytes = L.kq_attention_bytes(tq, nseq, heads, kv_heads, d, max_q)
+    work = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+    _check(L.kq_attention(_ptr(q), *_heads(q, "q"), _ptr(k), *_heads(k, "k"), _ptr(v),
+                          *_heads(v, "v"), _format(q.dtype), _ptr(cu_q), _ptr(cu_k), nseq, tq, tk,
+                          heads, kv_heads, d, max_q, 1 if causal else 0,
+                          d ** -0.5 if scale is None else scale, _ptr(out), *_heads(out, "out"),
+                          _ptr(stats), _ptr(work), _stream(stream)),
+           "kq_attention")
+    return (out, stats) if lse else out
