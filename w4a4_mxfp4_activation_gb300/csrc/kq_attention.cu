@@ -20,7 +20,7 @@
 // token's heads share one read of the cache and causal tiles waste little.
 //
 // Roles: warps 0-3 and 4-7 softmax of tile 0 and 1 (thread = row), warp 8
-// schedule and TMA loads, warp 9 MMAs.
+// schedule and TMA loads, warp 9 MMAs (10 and 11 only give their registers away).
 // TMEM: scores of the tiles at columns 0 and 128 (P, 16-bit, over the first half
 // of its scores), O at 256 and 384.
 // Shared memory: Q of both tiles, and a ring of K and V tiles of 128 keys
@@ -44,7 +44,10 @@
 namespace kq {
 namespace {
 
-constexpr int kAThreads = 320;
+constexpr int kAThreads = 384;                    // three warpgroups
+// Registers a thread: a softmax thread holds a row of 128 scores.  The launch gives
+// 168 to each of the 384; 256 * 216 + 128 * 72 = 384 * 168.
+constexpr int kARegsSoftmax = 216, kARegsOther = 72;
 constexpr int kABoxBytes = 128 * 128;            // 128 rows x 64 elements
 constexpr int kASlotRows = 256;                  // rows of one part in the workspace
 constexpr float kRescale = 8.0f;                 // log2 of the headroom of p
@@ -235,6 +238,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kARegsOther)); }
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kARegsSoftmax)); }
+
 // ---- the kernel ------------------------------------------------------------------------
 
 template <int DA, bool F16>
@@ -300,6 +306,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
 
     if (warp == 8) {
         // schedule and loads
+        regs_dec();
         Cursor cur;
         int64_t w = blockIdx.x, end = 0, quota = 0;
         if (g.split) {
@@ -378,6 +385,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         __syncwarp();
     } else if (warp == 9) {
         // MMAs: one elected lane issues, the warp waits converged
+        regs_dec();
         const bool leader = elect_one();
         constexpr uint32_t kFmt = F16 ? 0u : ((1u << 7) | (1u << 10));
         const uint32_t nv = static_cast<uint32_t>((g.d + 15) & ~15);
@@ -464,7 +472,10 @@ __global__ void __launch_bounds__(kAThreads, 1)
         if (leader) g_commit(drain);
         __syncwarp();
         (void)mbar_wait(drain, 0);
-    } else if (warp < 8) {
+    } else if (warp >= 10) {
+        regs_dec();
+    } else {
+        regs_inc();
         const int t = warp >> 2, qtr = warp & 3;
         const int r = qtr * 32 + lane;                   // row of the tile
         const int rt = r / g.gp, rh = r - rt * g.gp;     // its token and head in the tile
