@@ -20,7 +20,10 @@
 // token's heads share one read of the cache and causal tiles waste little.
 //
 // Roles: warps 0-3 and 4-7 softmax of tile 0 and 1 (thread = row), warp 8
-// schedule and TMA loads, warp 9 MMAs (10 and 11 only give their registers away).
+// schedule and TMA loads, warp 9 the MMAs (10 and 11 only give their registers
+// away).  Issuing an MMA costs its warp about as long as the tensor cores take for
+// it, hence straight-line code on warp-uniform operands.  (A warp of its own for each
+// tile's MMAs was slower: 1223 against 1106 us on the 16384-token prompt.)
 // TMEM: scores of the tiles at columns 0 and 128 (P, 16-bit, over the first half
 // of its scores), O at 256 and 384.
 // Shared memory: Q of both tiles, and a ring of K and V tiles of 128 keys
@@ -238,6 +241,27 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
+// N words of a row, `left` bytes of them real (a multiple of 16): 32 bytes a store
+// where the row allows it.  Every lane writes its own row, so what counts is the
+// number of store instructions and whole 32-byte sectors.
+template <int N>
+__device__ __forceinline__ void store_row(uint8_t *dst, const uint32_t *o, int left, bool wide)
+{
+#pragma unroll
+    for (int k = 0; k < N; k += 8) {
+        if (wide && 4 * k + 32 <= left) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 4 * k),
+                         KQ_I8(o, k)
+                         : "memory");
+        } else {
+            if (4 * k < left)
+                *reinterpret_cast<uint4 *>(dst + 4 * k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+            if (4 * k + 16 < left)
+                *reinterpret_cast<uint4 *>(dst + 4 * k + 16) = make_uint4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
+        }
+    }
+}
+
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kARegsOther)); }
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kARegsSoftmax)); }
 
@@ -256,9 +280,10 @@ __global__ void __launch_bounds__(kAThreads, 1)
     const uint32_t bar = base + C::kBarOff;
     const uint32_t kv_full = bar, kv_empty = bar + 8 * C::kStages;
     const uint32_t b1 = bar + 16 * C::kStages;
-    const uint32_t q_full = b1, q_empty = b1 + 8, s_full = b1 + 16, p_ready = b1 + 32;
-    const uint32_t o_full = b1 + 48, seg_full = b1 + 64, seg_empty = b1 + 80, drain = b1 + 96;
-    const uint32_t tmem_slot = b1 + 104;
+    // per tile: Q, scores, P (in halves), O; then the two segment buffers
+    const uint32_t q_full = b1, q_empty = b1 + 16, s_full = b1 + 32, p_ready = b1 + 48, o_full = b1 + 80;
+    const uint32_t drain = b1 + 96, seg_full = b1 + 112, seg_empty = b1 + 128;
+    const uint32_t tmem_slot = b1 + 144;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -269,24 +294,26 @@ __global__ void __launch_bounds__(kAThreads, 1)
             mbar_init(kv_full + 8 * s, 1);
             mbar_init(kv_empty + 8 * s, 1);
         }
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
         for (int q = 0; q < 2; ++q) {
+            mbar_init(q_full + 8 * q, 1);
+            mbar_init(q_empty + 8 * q, 1);
             mbar_init(s_full + 8 * q, 1);
-            mbar_init(p_ready + 8 * q, 4);               // the softmax warps
+            mbar_init(p_ready + 16 * q, 4);              // the softmax warps
+            mbar_init(p_ready + 16 * q + 8, 4);
             mbar_init(o_full + 8 * q, 1);
+            mbar_init(drain + 8 * q, 1);
             mbar_init(seg_full + 8 * q, 1);
             mbar_init(seg_empty + 8 * q, 9);             // MMA and softmax warps
         }
-        mbar_init(drain, 1);
         mbar_fence_init();
     }
     if (warp == 9) g_tmem_alloc(tmem_slot, 512);
     g_fence_before();
     __syncthreads();
     g_fence_after();
-    uint32_t tmem;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
+    // All 512 columns are this CTA's, so they start at column 0: as a constant the
+    // address costs the MMA warps no register traffic.
+    constexpr uint32_t tmem = 0;
     grid_dependency_wait();
 
     // A role's segments: slot i of the pair of segment buffers.  False: no more
@@ -297,7 +324,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         s = segs[i & 1];
         __syncwarp();
         if (lane == 0) mbar_arrive(seg_empty + 8 * (i & 1));
-        return s.valid != 0;
+        return __shfl_sync(0xffffffffu, s.valid, 0) != 0;
     };
     // Key tiles of the segment that tile t works on.
     auto tiles_of = [&](const Segment &s, int t) {
@@ -318,7 +345,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             end = min(all.base, w + quota);
         }
         const int64_t begin = w;
-        int kv = 0, qn = 0;                              // stages and Q loads issued
+        int kv = 0, qn[2] = {0, 0};                      // stages and Q tiles loaded
         bool ok = true;
         for (int i = 0; ok; ++i) {
             Segment s;
@@ -350,21 +377,22 @@ __global__ void __launch_bounds__(kAThreads, 1)
             if (n == 0) continue;
             if (lane == 0) {
                 const int kvh = s.unit * g.gp / g.group, h0 = s.unit * g.gp;
-                if (qn > 0) ok = mbar_wait(q_empty, static_cast<uint32_t>((qn - 1) & 1));
-                if (ok) {
-                    const uint32_t box = static_cast<uint32_t>(g.gp * g.tpt) * 128u;
-                    mbar_arrive_expect_tx(q_full, box * DA * ((n0 > 0) + (n1 > 0)));
-                    for (int t = 0; t < 2; ++t) {
-                        if ((t ? n1 : n0) == 0) continue;
-                        for (int a = 0; a < DA; ++a)
-                            tma_load_3d(base + t * C::kTile + a * kABoxBytes, &tmQ, 64 * a, h0,
-                                        s.q0 + s.t0 + t * g.tpt, q_full);
-                    }
-                    ++qn;
-                }
+                const uint32_t box = static_cast<uint32_t>(g.gp * g.tpt) * 128u;
+                auto load_q = [&](int t) {
+                    if ((t ? n1 : n0) == 0 || !ok) return;
+                    if (qn[t] > 0) ok = mbar_wait(q_empty + 8 * t, static_cast<uint32_t>((qn[t] - 1) & 1));
+                    if (!ok) return;
+                    mbar_arrive_expect_tx(q_full + 8 * t, box * DA);
+                    for (int a = 0; a < DA; ++a)
+                        tma_load_3d(base + t * C::kTile + a * kABoxBytes, &tmQ, 64 * a, h0,
+                                    s.q0 + s.t0 + t * g.tpt, q_full + 8 * t);
+                    ++qn[t];
+                };
+                load_q(0);
                 for (int j = 0; j < 2 * n && ok; ++j, ++kv) {
+                    if (j == 1) load_q(1);               // after the first K: tile 0 can start
                     const int st = kv % C::kStages;
-                    if (kv >= C::kStages)
+                    if (ok && kv >= C::kStages)
                         ok = mbar_wait(kv_empty + 8 * st, static_cast<uint32_t>((kv / C::kStages - 1) & 1));
                     if (!ok) break;
                     const uint32_t dst = ring + static_cast<uint32_t>(st) * C::kTile;
@@ -378,93 +406,142 @@ __global__ void __launch_bounds__(kAThreads, 1)
         }
         if (lane == 0) {
             // no copy is in flight when the CTA leaves
-            if (qn > 0) (void)mbar_wait(q_full, static_cast<uint32_t>((qn - 1) & 1));
+            for (int t = 0; t < 2; ++t)
+                if (qn[t] > 0) (void)mbar_wait(q_full + 8 * t, static_cast<uint32_t>((qn[t] - 1) & 1));
             for (int j = max(0, kv - C::kStages); j < kv; ++j)
                 (void)mbar_wait(kv_full + 8 * (j % C::kStages), static_cast<uint32_t>((j / C::kStages) & 1));
         }
         __syncwarp();
     } else if (warp == 9) {
-        // MMAs: one elected lane issues, the warp waits converged
+        // MMAs: one elected lane issues, the warp waits converged.  Its operands are
+        // warp-uniform and its full tiles straight-line code.
         regs_dec();
         const bool leader = elect_one();
         constexpr uint32_t kFmt = F16 ? 0u : ((1u << 7) | (1u << 10));
+        constexpr uint32_t id_qk = (1u << 4) | kFmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
         const uint32_t nv = static_cast<uint32_t>((g.d + 15) & ~15);
-        const uint32_t id_qk = (1u << 4) | kFmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
         const uint32_t id_pv = (1u << 4) | kFmt | (1u << 16) | ((nv >> 3) << 17) | ((128u >> 4) << 24);
         const int ksteps = (g.d + 15) >> 4;
-        int kv = 0, qn = 0, pn[2] = {0, 0};              // stages, Q tiles, P tiles consumed
+        const bool full_d = ksteps == 4 * DA;
+        int st = 0;                                      // ring stage, its parity
+        uint32_t par = 0;
+        uint32_t qpar[2] = {0, 0}, ppar[2] = {0, 0};
         bool ok = true;
-        auto wait = [&](uint32_t b, uint32_t par) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(b, par));
+        auto wait = [&](uint32_t b, uint32_t p) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(b, p));
             g_fence_after();
         };
-        auto full = [&](int n) { wait(kv_full + 8 * (n % C::kStages), static_cast<uint32_t>((n / C::kStages) & 1)); };
-        auto stage = [&](int n) { return ring + static_cast<uint32_t>(n % C::kStages) * C::kTile; };
-        auto qk = [&](int t, int n) {
-            if (leader && ok) {
-                const uint32_t sq = base + t * C::kTile, sk = stage(n);
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint32_t off = static_cast<uint32_t>((k >> 2) * kABoxBytes + (k & 3) * 32);
-                    g_mma_id(tmem + 128 * t, g_desc(sq + off), g_desc(sk + off), id_qk, k > 0);
+        auto advance = [&] {
+            if (++st == C::kStages) {
+                st = 0;
+                par ^= 1;
+            }
+        };
+        // S = Q K^T of tile t from the K tile of stage `k`
+        auto qk = [&](int t, int k) {
+            const uint32_t ts = tmem + 128 * t;
+            const uint64_t dq = g_desc(base + t * C::kTile), dk = g_desc(ring + static_cast<uint32_t>(k) * C::kTile);
+            if (leader) {
+                if (full_d) {
+#pragma unroll
+                    for (int i = 0; i < 4 * DA; ++i) {
+                        const int off = (i >> 2) * (kABoxBytes >> 4) + (i & 3) * 2;
+                        g_mma_id(ts, dq + off, dk + off, id_qk, i > 0);
+                    }
+                } else {
+                    for (int i = 0; i < ksteps; ++i) {
+                        const int off = (i >> 2) * (kABoxBytes >> 4) + (i & 3) * 2;
+                        g_mma_id(ts, dq + off, dk + off, id_qk, i > 0);
+                    }
                 }
                 g_commit(s_full + 8 * t);
             }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t b) {
+            if (leader) g_commit(b);
+            __syncwarp();
         };
         Segment s;
         for (int i = 0; ok && take(i, s); ++i) {
-            const int nq[2] = {tiles_of(s, 0), tiles_of(s, 1)}, n = max(nq[0], nq[1]);
+            const int n0 = __shfl_sync(0xffffffffu, tiles_of(s, 0), 0);
+            const int n1 = __shfl_sync(0xffffffffu, tiles_of(s, 1), 0), n = max(n0, n1);
+            const int tail = __shfl_sync(0xffffffffu, s.klen - s.j0 * 128, 0);   // keys from tile j0 on
             if (n == 0) continue;
-            wait(q_full, static_cast<uint32_t>(qn & 1));
-            ++qn;
-            full(kv);
-            for (int t = 0; t < 2; ++t)
-                if (nq[t] > 0) qk(t, kv);
-            if (leader && ok) {
-                g_commit(kv_empty + 8 * (kv % C::kStages));
-                if (n == 1) g_commit(q_empty);
+            wait(kv_full + 8 * st, par);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if ((t ? n1 : n0) == 0) continue;
+                wait(q_full + 8 * t, qpar[t]);
+                qpar[t] ^= 1;
+                if (!ok) break;
+                qk(t, st);
+                if ((t ? n1 : n0) == 1) release(q_empty + 8 * t);
             }
-            ++kv;
+            if (!ok) break;
+            release(kv_empty + 8 * st);
+            advance();
             for (int j = 0; j < n && ok; ++j) {
-                const int nk = kv + 1;                   // the next K tile's stage
-                const uint32_t sv = stage(kv);
-                full(kv);
+                const int sv = st;
+                wait(kv_full + 8 * sv, par);
+                advance();
+                const uint32_t va = ring + static_cast<uint32_t>(sv) * C::kTile;
                 // keys of this tile; rows of V past the last one (another sequence's)
                 // could hold NaN, which a weight of zero does not undo: the MMAs stop
                 // at the next 16 keys, and the rows up to there are cleared
-                const int keys = min(128, s.klen - (s.j0 + j) * 128);
+                const int keys = min(128, tail - j * 128);
                 const int vsteps = (keys + 15) >> 4;
-                if (keys & 15) {
+                if (ok && (keys & 15)) {
                     const int pad = vsteps * 16 - keys;
                     for (int c = lane; c < pad * 8 * DA; c += 32) {
                         const int row = keys + (c >> 3) % pad, box = (c >> 3) / pad;
-                        sts128(sv + box * kABoxBytes + row * 128 + (c & 7) * 16, make_uint4(0, 0, 0, 0));
+                        sts128(va + box * kABoxBytes + row * 128 + (c & 7) * 16, make_uint4(0, 0, 0, 0));
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
+                const uint64_t dv = a_desc_v(va);
+                bool next = false;                       // the next K tile has been waited for
+#pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (j < nq[t]) {
-                        wait(p_ready + 8 * t, static_cast<uint32_t>(pn[t] & 1));
-                        ++pn[t];
-                        if (leader && ok) {
-                            for (int k = 0; k < vsteps; ++k)
-                                a_mma_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k,
-                                         a_desc_v(sv + 2048 * k), id_pv, (j > 0 || k > 0) ? 1u : 0u);
-                            if (j == nq[t] - 1) g_commit(o_full + 8 * t);
+                    const int mine = t ? n1 : n0;
+                    if (j < mine) {
+                        const uint32_t ts = tmem + 128 * t, to = tmem + 256 + 128 * t;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            wait(p_ready + 16 * t + 8 * h, ppar[t]);
+                            if (!ok) break;
+                            const uint32_t acc = j > 0 || h > 0;
+                            if (leader) {
+                                if (vsteps == 8) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k)
+                                        a_mma_ts(to, ts + 32 * h + 8 * k, dv + 512 * h + 128 * k, id_pv,
+                                                 k > 0 ? 1u : acc);
+                                } else {
+                                    for (int k = 0; k < 4 && 4 * h + k < vsteps; ++k)
+                                        a_mma_ts(to, ts + 32 * h + 8 * k, dv + 512 * h + 128 * k, id_pv,
+                                                 k > 0 ? 1u : acc);
+                                }
+                                if (h == 1 && j == mine - 1) g_commit(o_full + 8 * t);
+                            }
+                            __syncwarp();
                         }
+                        ppar[t] ^= 1;
                     }
-                    if (t == 1 && leader && ok) g_commit(kv_empty + 8 * (kv % C::kStages));
-                    if (j + 1 < n && t == 0) full(nk);
-                    if (j + 1 < nq[t]) qk(t, nk);
+                    if (t == 1) release(kv_empty + 8 * sv);
+                    if (j + 1 < mine) {
+                        if (!next) wait(kv_full + 8 * st, par);
+                        next = true;
+                        if (!ok) break;
+                        qk(t, st);
+                        if (j + 2 == mine) release(q_empty + 8 * t);
+                    }
                 }
                 if (j + 1 < n) {
-                    if (leader && ok) {
-                        g_commit(kv_empty + 8 * (nk % C::kStages));
-                        if (j + 2 == n) g_commit(q_empty);
-                    }
-                    kv += 2;
-                } else {
-                    kv += 1;
+                    if (!next) wait(kv_full + 8 * st, par);
+                    release(kv_empty + 8 * st);
+                    advance();
                 }
             }
         }
@@ -481,7 +558,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         const int rt = r / g.gp, rh = r - rt * g.gp;     // its token and head in the tile
         const uint32_t lanes = static_cast<uint32_t>(qtr * 32) << 16;
         const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
-        const uint32_t sbar = s_full + 8 * t, pbar = p_ready + 8 * t, obar = o_full + 8 * t;
+        const uint32_t sbar = s_full + 8 * t, pbar = p_ready + 16 * t, obar = o_full + 8 * t;
         int sn = 0, on = 0;                              // scores and outputs consumed
         bool ok = true;
         Segment s;
@@ -508,17 +585,51 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     for (int c = 0; c < 128; ++c)
                         if (c >= lim) v[c] = 0xFF800000u;
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float top = -INFINITY;
+                // weights of 64 keys against the maximum m, and their sums
+                const float2 sc = make_float2(g.scale_log2, g.scale_log2);
+                float2 sum[2];
+                uint32_t p[32];
+                auto weights = [&](int h) {
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    const float2 rf = make_float2(-ref, -ref);
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int c = 0; c < 128; c += 8) {
+                    for (int c = 0; c < 32; ++c) {
+                        const int e = 64 * h + 2 * c;
+                        float2 x = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                        x = __ffma2_rn(x, sc, rf);
+                        x.x = ex2_approx(x.x);
+                        x.y = ex2_approx(x.y);
+                        sum[c & 1] = __fadd2_rn(sum[c & 1], x);
+                        p[c] = pack16(x.x, x.y, F16);
+                    }
+                };
+                auto maximum = [&] {
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mx[k] = fmax3(mx[k], __uint_as_float(v[c + 2 * k]), __uint_as_float(v[c + 2 * k + 1]));
-                }
-                const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * g.scale_log2;
-                const bool raise = top > m + kRescale;   // also from m = -inf
-                if (__any_sync(0xffffffffu, raise)) {
-                    const float mn = raise ? top : m;
+                    for (int c = 0; c < 128; c += 8) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            mx[k] = fmax3(mx[k], __uint_as_float(v[c + 2 * k]), __uint_as_float(v[c + 2 * k + 1]));
+                    }
+                    top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * g.scale_log2;
+                };
+                auto hand_over = [&](int h) {
+                    a_st32(ts + 32 * h, p);
+                    a_wait_st();
+                    g_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pbar + 8 * h);
+                };
+                // The first half's weights are computed against the old maximum
+                // while the new one is found (the exponentials and the comparisons
+                // use different pipes); they are computed again in the rare tile
+                // that raises it.
+                weights(0);
+                maximum();
+                if (__any_sync(0xffffffffu, top > m + kRescale)) {   // also from m = -inf
+                    const float mn = top > m + kRescale ? top : m;
                     const float f = m == -INFINITY ? 0.f : ex2_approx(m - mn);
                     m = mn;
                     l *= f;
@@ -532,30 +643,13 @@ __global__ void __launch_bounds__(kAThreads, 1)
                             a_st32(to + c, o);
                         }
                     }
-                }
-                const float ref = m == -INFINITY ? 0.f : m;
-                const float2 sc = make_float2(g.scale_log2, g.scale_log2), rf = make_float2(-ref, -ref);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        const int e = 64 * h + 2 * c;
-                        float2 x = make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-                        x = __ffma2_rn(x, sc, rf);
-                        x.x = ex2_approx(x.x);
-                        x.y = ex2_approx(x.y);
-                        sum[c & 1] = __fadd2_rn(sum[c & 1], x);
-                        p[c] = pack16(x.x, x.y, F16);
-                    }
-                    a_st32(ts + 32 * h, p);
+                    weights(0);
                 }
                 l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-                a_wait_st();
-                g_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pbar);
+                hand_over(0);
+                weights(1);
+                l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+                hand_over(1);
             }
             if (!ok) break;
             if (n > 0) {
@@ -569,6 +663,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
             const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             const int64_t row = s.q0 + tok;
             const int head = s.unit * g.gp + rh;
+            // rows of the output start on 32 bytes (the workspace's always do)
+            const bool wide = ((reinterpret_cast<uintptr_t>(g.out) & 31) | ((g.out_token | g.out_head) & 15)) == 0;
             uint8_t *dst;
             if (s.slot < 0) {
                 dst = static_cast<uint8_t *>(g.out) + (row * g.out_token + head * g.out_head) * 2;
@@ -589,19 +685,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 }
                 if (!real) continue;
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    if (c + k >= g.d) break;
-                    float f[8];
+                for (int k = 0; k < 32; ++k)
+                    o[k] = __float_as_uint(inv == 0.f ? 0.f : __uint_as_float(o[k]) * inv);
+                if (s.slot < 0) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = inv == 0.f ? 0.f : __uint_as_float(o[k + e]) * inv;
-                    if (s.slot < 0) {
-                        *reinterpret_cast<uint4 *>(dst + (c + k) * 2) =
-                            make_uint4(pack16(f[0], f[1], F16), pack16(f[2], f[3], F16),
-                                       pack16(f[4], f[5], F16), pack16(f[6], f[7], F16));
-                    } else {
-                        stg_f4(reinterpret_cast<float *>(dst) + c + k, make_float4(f[0], f[1], f[2], f[3]));
-                        stg_f4(reinterpret_cast<float *>(dst) + c + k + 4, make_float4(f[4], f[5], f[6], f[7]));
-                    }
+                    for (int k = 0; k < 16; ++k)
+                        o[k] = pack16(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]), F16);
+                    store_row<16>(dst + c * 2, o, (g.d - c) * 2, wide);
+                } else {
+                    store_row<32>(dst + c * 4, o, (g.d - c) * 4, true);
                 }
             }
             g_fence_before();
@@ -611,7 +703,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
     __syncthreads();
     if (warp == 9) {
         g_fence_after();
-        g_tmem_dealloc(tmem, 512);
+        uint32_t addr;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(addr) : "r"(tmem_slot) : "memory");
+        g_tmem_dealloc(addr, 512);
     }
 }
 
