@@ -154,6 +154,18 @@ def test_whole_items_on_every_sm(causal):
 
 
 @gpu
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("heads,kv_heads,lq,lk", [
+    (2, 2, [2000, 300, 0, 1500], [2000, 700, 9, 1500]),     # shares of tile pairs
+    (8, 2, [1000, 1, 129], [3000, 2500, 129]),
+    (24, 24, [700], [700]),
+    (1, 1, [2050], [2050])])
+def test_shares_of_tile_pairs(heads, kv_heads, lq, lk, causal):
+    """Fewer tile pairs than SMs, at both sides of the choice of single tiles."""
+    run(lq, lk, heads, kv_heads, 64, torch.bfloat16, causal, seed=heads)
+
+
+@gpu
 def test_scale_and_growing_scores():
     """Scores that grow along the keys raise the running maximum in every tile,
     and a small scale leaves all weights alike."""
@@ -223,15 +235,27 @@ def test_offsets_out_of_range_are_clamped():
 
 
 @gpu
-def test_empty_hint_stream_and_repeatable():
+@pytest.mark.parametrize("tq,cu", [(64, [0, 64, 0, 64, 0, 64]), (3, [0, 3] * 60), (300, [300, 0, 300, 100])])
+def test_falling_offsets_stay_in_range(tq, cu):
+    """Offsets that fall are an error of the caller's: the result is not defined,
+    but nothing outside the outputs is touched."""
+    q, k, v = make([tq], [tq], 2, 2, 64, torch.bfloat16, 7)
+    buf = torch.full((tq + 64, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    kq.kq_attention(q, k, v, cu, cu, out=buf[:tq])
+    torch.cuda.synchronize()
+    assert (buf[tq:] == 7.0).all()
+
+
+@gpu
+def test_empty_bounds_stream_and_repeatable():
     e = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     assert kq.kq_attention(e, e, e, offsets([0]), offsets([0]), 0).shape == (0, 4, 64)
     lq, lk = [1, 4, 300], [3000, 90, 300]
     q, k, v = make(lq, lk, 8, 2, 128, torch.bfloat16, 11)
     first, _ = run(lq, lk, 8, 2, 128, torch.bfloat16, True, seed=11)
-    # a wrong bound of the query lengths changes the schedule, not the result's bounds
-    out, lse = kq.kq_attention(q, k, v, offsets(lq), offsets(lk), 1, lse=True)
-    check(out, lse, q, k, v, lq, lk, True)
+    # the bounds of the lengths are not used: wrong ones change nothing
+    assert torch.equal(first, kq.kq_attention(q, k, v, offsets(lq), offsets(lk), 1, 1))
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
@@ -254,17 +278,17 @@ FAKE = 1 << 20
 
 
 def _att(q=FAKE, qs=(256, 64), k=FAKE, ks=(128, 64), v=FAKE, vs=(128, 64), fmt=0, cu_q=FAKE, cu_k=FAKE,
-         nseq=2, tq=8, tk=8, heads=4, kv=2, d=64, max_q=8, causal=1, scale=0.125, out=FAKE, os=(256, 64),
+         nseq=2, tq=8, tk=8, heads=4, kv=2, d=64, causal=1, scale=0.125, out=FAKE, os=(256, 64),
          lse=None, work=FAKE):
     return kq.lib().kq_attention(q, *qs, k, *ks, v, *vs, fmt, cu_q, cu_k, nseq, tq, tk, heads, kv, d,
-                                 max_q, causal, scale, out, *os, lse, work, None)
+                                 causal, scale, out, *os, lse, work, None)
 
 
 def test_argument_checks():
     assert _att(fmt=2) == 4 and _att(fmt=-1) == 4
     assert _att(d=60) == 2 and _att(d=0) == 2 and _att(d=136) == 2 and _att(heads=3) == 2
     assert _att(kv=0) == 2 and _att(tq=-1) == 2 and _att(tk=-1) == 2 and _att(nseq=-1) == 2
-    assert _att(max_q=-1) == 2 and _att(tq=1 << 31) == 2 and _att(heads=1 << 17, kv=1 << 16) == 2
+    assert _att(tq=1 << 31) == 2 and _att(heads=1 << 17, kv=1 << 16) == 2
     assert _att(scale=0.0) == 2 and _att(scale=-1.0) == 2 and _att(scale=float("nan")) == 2
     assert _att(scale=float("inf")) == 2
     assert _att(qs=(256, 32)) == 2 and _att(ks=(32, 64)) == 2 and _att(os=(0, 64)) == 2
@@ -278,9 +302,9 @@ def test_argument_checks():
 
 def test_workspace_bytes():
     size = kq.lib().kq_attention_bytes
-    assert size(0, 2, 4, 2, 64, 8) == 0 and size(8, 2, 4, 3, 64, 8) == 0 and size(8, 2, 4, 2, 60, 8) == 0
-    assert size(8, 8, 32, 8, 128, 1) > 0                     # few items: split
-    assert size(16384, 1, 24, 24, 128, 16384) == 0           # whole items fill the SMs
+    assert size(0, 2, 4, 2, 64) == 0 and size(8, 2, 4, 3, 64) == 0 and size(8, 2, 4, 2, 60) == 0
+    assert size(8, 8, 32, 8, 128) > 0                        # few items: split
+    assert size(16384, 1, 24, 24, 128) == 0                  # whole items fill the SMs
 
 
 def test_binding_refusals():

@@ -30,10 +30,15 @@
 // (K_0 V_0 K_1 V_1 ...), rows of 128 bytes in the 128-byte swizzle.
 //
 // Schedule: persistent CTAs.  With many items (tile pair x key/value head), a CTA
-// takes whole items, long ones first, in an order that alternates direction from
-// round to round.  With fewer items than SMs, all items' key tiles are laid end to
-// end and cut into equal shares; an item cut by a share's border leaves
-// normalised parts and their lse in the workspace, and a second kernel joins them.
+// takes whole items: the last tile pairs of all sequences first, then the ones
+// before them, ..., in rounds of alternating direction, so that lengths even out.
+// With fewer items than SMs, all items' key tiles are laid end to end and cut into
+// equal shares; an item cut by a share's border leaves normalised parts and their
+// lse in the workspace, and a second kernel joins them.  When even single tiles are
+// fewer than SMs (one new token per sequence), items are single tiles and the two
+// warpgroups take alternate key tiles of the same queries: the chain of product,
+// softmax and product takes longer than a key tile's way from HBM, and two chains
+// hide it.  Each warpgroup then leaves a part.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -72,12 +77,15 @@ struct AttnArgs {
     int tpt;                      // tokens per tile
     int units;                    // heads / gp: items per tile pair
     int d;
-    int causal, split;
+    int causal;
+    int split, alt;               // shares of key tiles; single tiles, alternate key tiles
+    int span;                     // tokens per item: 2 tpt, or tpt (alt)
     float scale_log2;
     void *out;
     int64_t out_token, out_head;  // strides in elements
     float *lse;                   // [tq][heads] or null
-    float *part, *part_lse;       // workspace of the split schedule
+    float *part, *part_lse;       // workspace of the split schedules
+    int slots;                    // parts it holds
 };
 
 // One piece of work: query tokens q0 + t0 .. of a sequence against its key tiles
@@ -92,81 +100,165 @@ struct Segment {
 };
 
 // Key tiles that some row of tile t (tokens t0 + t * tpt ...) sees.
-__device__ __forceinline__ int tile_limit(const AttnArgs &g, int qlen, int klen, int t0, int t)
+__device__ __forceinline__ int tile_limit(const AttnArgs &g, const Segment &s, int t)
 {
-    const int first = t0 + t * g.tpt;
-    if (first >= qlen) return 0;
-    int seen = klen;
-    if (g.causal) seen = min(klen, min(qlen, first + g.tpt) + klen - qlen);
+    const int first = s.t0 + t * g.tpt;
+    if (first >= s.qlen) return 0;
+    int seen = s.klen;
+    if (g.causal) seen = min(s.klen, min(s.qlen, first + g.tpt) + s.klen - s.qlen);
     return seen > 0 ? (seen + 127) >> 7 : 0;
 }
 
-// A warp's cursor over the sequences, 32 at a time: finds the one that holds
-// position w of the running count of work (items, or key tiles of items).
-struct Cursor {
-    int b0 = -32;
-    int64_t base = 0, total = 0;  // count before and within the 32 sequences
-    int64_t incl = 0;             // count up to and with this lane's sequence
+// Key tiles of the segment that tile (or, alt, warpgroup) t works on.
+__device__ __forceinline__ int tiles_of(const AttnArgs &g, const Segment &s, int t)
+{
+    if (!g.alt) return max(0, min(s.j1, tile_limit(g, s, t)) - s.j0);
+    const int n = max(0, min(s.j1, tile_limit(g, s, 0)) - s.j0);
+    return (n + 1 - t) >> 1;
+}
+
+// 32 sequences, one a lane, from number b0 on.  The offsets are the caller's:
+// whatever they hold, rows stay in range.
+struct Sequences {
     int q0 = 0, qlen = 0, k0 = 0, klen = 0;
-
-    __device__ __forceinline__ int pairs(const AttnArgs &g) const { return (qlen + 2 * g.tpt - 1) / (2 * g.tpt); }
-    __device__ __forceinline__ int tiles(const AttnArgs &g) const { return g.split ? max(1, (klen + 127) >> 7) : 1; }
-
-    __device__ __forceinline__ bool next(const AttnArgs &g)
+    __device__ __forceinline__ void load(const AttnArgs &g, int b0)
     {
-        base += total;
-        b0 += 32;
-        if (b0 >= g.nseq) {
-            total = 0;
-            return false;
-        }
         const int b = b0 + static_cast<int>(threadIdx.x & 31);
         q0 = qlen = k0 = klen = 0;
         if (b < g.nseq) {
-            // offsets are the caller's: whatever they hold, rows stay in range
             q0 = min(max(__ldg(g.cu_q + b), 0), g.tq);
             qlen = max(min(__ldg(g.cu_q + b + 1), g.tq) - q0, 0);
             k0 = min(max(__ldg(g.cu_k + b), 0), g.tk);
             klen = max(min(__ldg(g.cu_k + b + 1), g.tk) - k0, 0);
         }
-        incl = static_cast<int64_t>(pairs(g)) * g.units * tiles(g);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (static_cast<int>(threadIdx.x & 31) >= o) incl += v;
-        }
-        total = __shfl_sync(0xffffffffu, incl, 31);
-        return true;
     }
-
-    // Position w, at or after the last one asked for: the segment it starts (one
-    // item, or its key tiles up to `end`).  False past the end.
-    __device__ __forceinline__ bool find(const AttnArgs &g, int64_t w, int64_t end, Segment &s)
+    __device__ __forceinline__ int spans(const AttnArgs &g) const
     {
-        while (w >= base + total)
-            if (!next(g)) return false;
-        const uint32_t hit = __ballot_sync(0xffffffffu, w < base + incl);
-        const int src = __ffs(hit) - 1;
+        return qlen > 0 ? (qlen - 1) / g.span + 1 : 0;
+    }
+    __device__ __forceinline__ void pick(int src, Segment &s) const
+    {
         s.q0 = __shfl_sync(0xffffffffu, q0, src);
         s.qlen = __shfl_sync(0xffffffffu, qlen, src);
         s.k0 = __shfl_sync(0xffffffffu, k0, src);
         s.klen = __shfl_sync(0xffffffffu, klen, src);
-        const int np = __shfl_sync(0xffffffffu, pairs(g), src), nt = __shfl_sync(0xffffffffu, tiles(g), src);
-        const int64_t before = base + __shfl_sync(0xffffffffu, incl, src) -
-                               static_cast<int64_t>(np) * g.units * nt;
-        const int64_t off = w - before;
-        const int item = static_cast<int>(off / nt);
-        s.t0 = (np - 1 - item / g.units) * 2 * g.tpt;      // the longest tiles first
-        s.unit = item % g.units;
+    }
+};
+
+// Whole items in the order of falling span number (for causal prompts: of falling
+// length): all sequences' items of span p, then those of p - 1.  A warp's cursor.
+struct LevelCursor {
+    Sequences seq;
+    int b0 = -1;                  // the sequences in seq
+    int p = 0;                    // current span number
+    int64_t base = 0, count = 0;  // items before it, and of it
+
+    __device__ __forceinline__ void at(const AttnArgs &g, int b)
+    {
+        if (b != b0) seq.load(g, b);
+        b0 = b;
+    }
+    __device__ __forceinline__ void start(const AttnArgs &g)
+    {
+        int most = 0;
+        for (int b = 0; b < g.nseq; b += 32) {
+            at(g, b);
+            most = max(most, __reduce_max_sync(0xffffffffu, seq.spans(g)));
+        }
+        p = most;
+    }
+    // Item w, at or after the last one asked for.  False past the end.
+    __device__ __forceinline__ bool find(const AttnArgs &g, int64_t w, Segment &s)
+    {
+        while (w >= base + count) {
+            base += count;
+            if (--p < 0) {
+                p = 0;
+                count = 0;
+                return false;
+            }
+            int n = 0;
+            for (int b = 0; b < g.nseq; b += 32) {
+                at(g, b);
+                n += __popc(__ballot_sync(0xffffffffu, seq.spans(g) > p));
+            }
+            count = static_cast<int64_t>(n) * g.units;
+        }
+        const int64_t off = w - base;
+        int64_t nth = off / g.units;
+        for (int b = 0; b < g.nseq; b += 32) {
+            at(g, b);
+            uint32_t has = __ballot_sync(0xffffffffu, seq.spans(g) > p);
+            const int n = __popc(has);
+            if (nth < n) {
+                for (; nth > 0; --nth) has &= has - 1;
+                seq.pick(__ffs(has) - 1, s);
+                break;
+            }
+            nth -= n;
+        }
+        s.t0 = p * g.span;
+        s.unit = static_cast<int>(off % g.units);
+        s.j0 = 0;
+        s.j1 = (s.klen + 127) >> 7;
         s.slot = -1;
         s.valid = 1;
-        if (!g.split) {
-            s.j0 = 0;
-            s.j1 = (s.klen + 127) >> 7;
-        } else {
-            s.j0 = static_cast<int>(off % nt);
-            s.j1 = static_cast<int>(min(static_cast<int64_t>(nt), s.j0 + (end - w)));
+        return true;
+    }
+};
+
+// The split schedules count key tiles, sequence by sequence and item by item (at
+// least one an item, so that rows without keys are written).  A warp's cursor.
+struct TileCursor {
+    Sequences seq;
+    int b0 = -32;
+    int64_t base = 0, total = 0, incl = 0;       // tiles before these sequences, of them, up to this lane's
+    int64_t ibase = 0, itotal = 0, iincl = 0;    // the same in items
+
+    __device__ __forceinline__ int tiles() const { return max(1, (seq.klen + 127) >> 7); }
+
+    __device__ __forceinline__ bool next(const AttnArgs &g)
+    {
+        base += total;
+        ibase += itotal;
+        b0 += 32;
+        total = itotal = 0;
+        if (b0 >= g.nseq) return false;
+        seq.load(g, b0);
+        iincl = static_cast<int64_t>(seq.spans(g)) * g.units;
+        incl = iincl * tiles();
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, incl, o), w = __shfl_up_sync(0xffffffffu, iincl, o);
+            if (static_cast<int>(threadIdx.x & 31) >= o) {
+                incl += v;
+                iincl += w;
+            }
         }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+        itotal = __shfl_sync(0xffffffffu, iincl, 31);
+        return true;
+    }
+
+    // The segment that starts at tile w (at or after the last one asked for), up
+    // to its item's end or tile `end`; `item`: its item's number.
+    __device__ __forceinline__ bool find(const AttnArgs &g, int64_t w, int64_t end, Segment &s, int64_t &item)
+    {
+        while (w >= base + total)
+            if (!next(g)) return false;
+        const int src = __ffs(__ballot_sync(0xffffffffu, w < base + incl)) - 1;
+        seq.pick(src, s);
+        const int np = __shfl_sync(0xffffffffu, seq.spans(g), src), nt = __shfl_sync(0xffffffffu, tiles(), src);
+        const int64_t items = static_cast<int64_t>(np) * g.units;
+        const int64_t off = w - (base + __shfl_sync(0xffffffffu, incl, src) - items * nt);
+        const int in = static_cast<int>(off / nt);
+        item = ibase + __shfl_sync(0xffffffffu, iincl, src) - items + in;
+        s.t0 = in / g.units * g.span;
+        s.unit = in % g.units;
+        s.j0 = static_cast<int>(off % nt);
+        s.j1 = static_cast<int>(min(static_cast<int64_t>(nt), s.j0 + (end - w)));
+        s.slot = -1;
+        s.valid = 1;
         return true;
     }
 };
@@ -231,6 +323,22 @@ __device__ __forceinline__ void a_wait_ld(uint32_t *r)
 }
 __device__ __forceinline__ void a_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Eight columns times f, in place (few registers: the caller holds a row of scores).
+__device__ __forceinline__ void scale8(uint32_t taddr, float f)
+{
+    uint32_t o[8];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : KQ_R8(o, 0)
+                 : "r"(taddr)
+                 : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : KQ_IO8(o, 0) : : "memory");
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+                 KQ_I8(o, 0)
+                 : "memory");
+}
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y,
                                             int32_t z, uint32_t bar)
 {
@@ -241,25 +349,27 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
         : "memory");
 }
 
-// N words of a row, `left` bytes of them real (a multiple of 16): 32 bytes a store
-// where the row allows it.  Every lane writes its own row, so what counts is the
-// number of store instructions and whole 32-byte sectors.
-template <int N>
-__device__ __forceinline__ void store_row(uint8_t *dst, const uint32_t *o, int left, bool wide)
+// 32 columns of O times `inv` (0 where a row has no keys, whatever O holds).
+__device__ __forceinline__ void load_o(uint32_t (&o)[32], uint32_t taddr, int n, float inv)
+{
+    if (n > 0) {
+        a_ld32(taddr, o);
+        a_wait_ld(o);
+    }
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+        o[k] = __float_as_uint(n == 0 || inv == 0.f ? 0.f : __uint_as_float(o[k]) * inv);
+}
+
+// 32 words of a part's row, `left` bytes of them real (a multiple of 32).
+__device__ __forceinline__ void store_row(uint8_t *dst, const uint32_t (&o)[32], int left)
 {
 #pragma unroll
-    for (int k = 0; k < N; k += 8) {
-        if (wide && 4 * k + 32 <= left) {
+    for (int k = 0; k < 32; k += 8)
+        if (4 * k < left)
             asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 4 * k),
                          KQ_I8(o, k)
                          : "memory");
-        } else {
-            if (4 * k < left)
-                *reinterpret_cast<uint4 *>(dst + 4 * k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-            if (4 * k + 16 < left)
-                *reinterpret_cast<uint4 *>(dst + 4 * k + 16) = make_uint4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]);
-        }
-    }
 }
 
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kARegsOther)); }
@@ -316,52 +426,52 @@ __global__ void __launch_bounds__(kAThreads, 1)
     constexpr uint32_t tmem = 0;
     grid_dependency_wait();
 
-    // A role's segments: slot i of the pair of segment buffers.  False: no more
-    // work, or the wait for it gave up.
-    auto take = [&](int i, Segment &s) {
+    // A role's segments, in two buffers: waits for number i (false: no more work, or
+    // the wait gave up), and gives its buffer back.
+    auto take = [&](int i) {
         if (!__all_sync(0xffffffffu, mbar_wait(seg_full + 8 * (i & 1), static_cast<uint32_t>((i >> 1) & 1))))
             return false;
-        s = segs[i & 1];
+        return __shfl_sync(0xffffffffu, segs[i & 1].valid, 0) != 0;
+    };
+    auto give_back = [&](int i) {
         __syncwarp();
         if (lane == 0) mbar_arrive(seg_empty + 8 * (i & 1));
-        return __shfl_sync(0xffffffffu, s.valid, 0) != 0;
-    };
-    // Key tiles of the segment that tile t works on.
-    auto tiles_of = [&](const Segment &s, int t) {
-        return max(0, min(s.j1, tile_limit(g, s.qlen, s.klen, s.t0, t)) - s.j0);
     };
 
     if (warp == 8) {
         // schedule and loads
         regs_dec();
-        Cursor cur;
-        int64_t w = blockIdx.x, end = 0, quota = 0;
+        LevelCursor items;
+        TileCursor tiles;
+        int64_t w = 0, end = 0, item = 0;
         if (g.split) {
-            Cursor all;
-            while (all.next(g)) {
+            while (tiles.next(g)) {
             }
-            quota = (all.base + gridDim.x - 1) / gridDim.x;
+            const int64_t quota = (tiles.base + gridDim.x - 1) / gridDim.x;
             w = static_cast<int64_t>(blockIdx.x) * quota;
-            end = min(all.base, w + quota);
+            end = min(tiles.base, w + quota);
+            tiles = TileCursor();
+        } else {
+            items.start(g);
         }
-        const int64_t begin = w;
         int kv = 0, qn[2] = {0, 0};                      // stages and Q tiles loaded
         bool ok = true;
         for (int i = 0; ok; ++i) {
             Segment s;
             if (!g.split) {
-                // round i, direction alternating: lengths even out over the rounds
                 w = static_cast<int64_t>(i) * gridDim.x +
                     ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                if (!cur.find(g, w, 0, s)) s.valid = 0;
+                if (!items.find(g, w, s)) s.valid = 0;
+            } else if (w >= end || !tiles.find(g, w, end, s, item)) {
+                s.valid = 0;
             } else {
-                if (w >= end || !cur.find(g, w, end, s)) {
-                    s.valid = 0;
-                } else {
-                    const int nt = max(1, (s.klen + 127) >> 7);
-                    if (s.j1 - s.j0 < nt) s.slot = static_cast<int>(blockIdx.x) * 2 + (w == begin ? 0 : 1);
-                    w += s.j1 - s.j0;
+                // Parts are numbered by item + CTA: both never fall from one part
+                // to the next, and one of them rises.
+                if (g.alt || s.j1 - s.j0 < max(1, (s.klen + 127) >> 7)) {
+                    s.slot = static_cast<int>(item) + static_cast<int>(blockIdx.x);
+                    if (s.slot >= g.slots) s.valid = 0;  // only if the offsets fall
                 }
+                w += s.j1 - s.j0;
             }
             if (i >= 2)
                 ok = __all_sync(0xffffffffu, mbar_wait(seg_empty + 8 * (i & 1),
@@ -373,14 +483,13 @@ __global__ void __launch_bounds__(kAThreads, 1)
             }
             __syncwarp();
             if (!s.valid) break;
-            const int n0 = tiles_of(s, 0), n1 = tiles_of(s, 1), n = max(n0, n1);
+            const int n0 = tiles_of(g, s, 0), n1 = tiles_of(g, s, 1), n = g.alt ? n0 + n1 : max(n0, n1);
             if (n == 0) continue;
             if (lane == 0) {
                 const int kvh = s.unit * g.gp / g.group, h0 = s.unit * g.gp;
                 const uint32_t box = static_cast<uint32_t>(g.gp * g.tpt) * 128u;
                 auto load_q = [&](int t) {
-                    if ((t ? n1 : n0) == 0 || !ok) return;
-                    if (qn[t] > 0) ok = mbar_wait(q_empty + 8 * t, static_cast<uint32_t>((qn[t] - 1) & 1));
+                    if (qn[t] > 0) ok = ok && mbar_wait(q_empty + 8 * t, static_cast<uint32_t>((qn[t] - 1) & 1));
                     if (!ok) return;
                     mbar_arrive_expect_tx(q_full + 8 * t, box * DA);
                     for (int a = 0; a < DA; ++a)
@@ -388,18 +497,33 @@ __global__ void __launch_bounds__(kAThreads, 1)
                                     s.q0 + s.t0 + t * g.tpt, q_full + 8 * t);
                     ++qn[t];
                 };
-                load_q(0);
-                for (int j = 0; j < 2 * n && ok; ++j, ++kv) {
-                    if (j == 1) load_q(1);               // after the first K: tile 0 can start
+                // key tile j of the segment's, of K or of V, into the next stage
+                auto load_kv = [&](const CUtensorMap *map, int j) {
                     const int st = kv % C::kStages;
-                    if (ok && kv >= C::kStages)
-                        ok = mbar_wait(kv_empty + 8 * st, static_cast<uint32_t>((kv / C::kStages - 1) & 1));
-                    if (!ok) break;
+                    if (kv >= C::kStages)
+                        ok = ok && mbar_wait(kv_empty + 8 * st, static_cast<uint32_t>((kv / C::kStages - 1) & 1));
+                    if (!ok) return;
                     const uint32_t dst = ring + static_cast<uint32_t>(st) * C::kTile;
                     mbar_arrive_expect_tx(kv_full + 8 * st, C::kTile);
                     for (int a = 0; a < DA; ++a)
-                        tma_load_3d(dst + a * kABoxBytes, (j & 1) ? &tmV : &tmK, 64 * a, kvh,
-                                    s.k0 + (s.j0 + (j >> 1)) * 128, kv_full + 8 * st);
+                        tma_load_3d(dst + a * kABoxBytes, map, 64 * a, kvh, s.k0 + (s.j0 + j) * 128,
+                                    kv_full + 8 * st);
+                    ++kv;
+                };
+                if (n0 > 0) load_q(0);
+                load_kv(&tmK, 0);
+                if (!g.alt) {
+                    if (n1 > 0) load_q(1);               // after the first K: tile 0 can start
+                    for (int j = 0; j < n && ok; ++j) {
+                        load_kv(&tmV, j);
+                        if (j + 1 < n) load_kv(&tmK, j + 1);
+                    }
+                } else {
+                    if (n > 1) load_kv(&tmK, 1);
+                    for (int j = 0; j < n && ok; ++j) {
+                        load_kv(&tmV, j);
+                        if (j + 2 < n) load_kv(&tmK, j + 2);
+                    }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -437,10 +561,10 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 par ^= 1;
             }
         };
-        // S = Q K^T of tile t from the K tile of stage `k`
-        auto qk = [&](int t, int k) {
+        // S = Q K^T into the scores of t, from Q tile qt and the K tile of stage `k`
+        auto qk = [&](int t, int qt, int k) {
             const uint32_t ts = tmem + 128 * t;
-            const uint64_t dq = g_desc(base + t * C::kTile), dk = g_desc(ring + static_cast<uint32_t>(k) * C::kTile);
+            const uint64_t dq = g_desc(base + qt * C::kTile), dk = g_desc(ring + static_cast<uint32_t>(k) * C::kTile);
             if (leader) {
                 if (full_d) {
 #pragma unroll
@@ -462,12 +586,91 @@ __global__ void __launch_bounds__(kAThreads, 1)
             if (leader) g_commit(b);
             __syncwarp();
         };
-        Segment s;
-        for (int i = 0; ok && take(i, s); ++i) {
-            const int n0 = __shfl_sync(0xffffffffu, tiles_of(s, 0), 0);
-            const int n1 = __shfl_sync(0xffffffffu, tiles_of(s, 1), 0), n = max(n0, n1);
+        // O (+)= P V of tile t from the V tile of stage `k`, which holds `keys` keys;
+        // rows of V past the last one (another sequence's) could hold NaN, which a
+        // weight of zero does not undo: the MMAs stop at the next 16 keys, and the
+        // rows up to there are cleared.  The weights come in halves of 64 keys.
+        auto clear_tail = [&](int k, int keys) {
+            if ((keys & 15) == 0) return;
+            const int pad = 16 - (keys & 15);
+            for (int c = lane; c < pad * 8 * DA; c += 32) {
+                const int row = keys + (c >> 3) % pad, box = (c >> 3) / pad;
+                sts128(ring + static_cast<uint32_t>(k) * C::kTile + box * kABoxBytes + row * 128 + (c & 7) * 16,
+                       make_uint4(0, 0, 0, 0));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        auto pv = [&](int t, int k, int keys, bool more, bool last) {
+            const uint32_t ts = tmem + 128 * t, to = tmem + 256 + 128 * t;
+            const uint64_t dv = a_desc_v(ring + static_cast<uint32_t>(k) * C::kTile);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                wait(p_ready + 16 * t + 8 * h, ppar[t]);
+                if (!ok) return;
+                const uint32_t acc = more || h > 0;
+                if (leader) {
+                    if (keys == 128) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            a_mma_ts(to, ts + 32 * h + 8 * i, dv + 512 * h + 128 * i, id_pv, i > 0 ? 1u : acc);
+                    } else {
+                        for (int i = 0; i < 4 && 64 * h + 16 * i < keys; ++i)
+                            a_mma_ts(to, ts + 32 * h + 8 * i, dv + 512 * h + 128 * i, id_pv, i > 0 ? 1u : acc);
+                    }
+                    if (h == 1 && last) g_commit(o_full + 8 * t);
+                }
+                __syncwarp();
+            }
+            ppar[t] ^= 1;
+        };
+        for (int i = 0; ok && take(i); ++i) {
+            const Segment &s = segs[i & 1];
+            const int n0 = __shfl_sync(0xffffffffu, tiles_of(g, s, 0), 0);
+            const int n1 = __shfl_sync(0xffffffffu, tiles_of(g, s, 1), 0);
             const int tail = __shfl_sync(0xffffffffu, s.klen - s.j0 * 128, 0);   // keys from tile j0 on
+            const bool whole = __shfl_sync(0xffffffffu, s.slot, 0) < 0;
+            const int n = g.alt ? n0 + n1 : max(n0, n1);
+            give_back(i);
             if (n == 0) continue;
+            if (g.alt) {
+                // one tile of queries; key tile j is warpgroup j & 1's
+                wait(q_full, qpar[0]);
+                qpar[0] ^= 1;
+                for (int j = 0; j < 2 && j < n && ok; ++j) {
+                    wait(kv_full + 8 * st, par);
+                    if (!ok) break;
+                    qk(j, 0, st);
+                    release(kv_empty + 8 * st);
+                    if (j == n - 1) release(q_empty);
+                    advance();
+                }
+                for (int j = 0; j < n && ok; j += 2) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {        // j + t: t is known to the compiler
+                        if (j + t >= n) break;
+                        wait(kv_full + 8 * st, par);
+                        if (!ok) break;
+                        const int keys = min(128, tail - (j + t) * 128);
+                        clear_tail(st, keys);
+                        pv(t, st, keys, j > 0, j + t + 2 >= n);
+                        if (!ok) break;
+                        release(kv_empty + 8 * st);
+                        advance();
+                        if (j + t + 2 < n) {
+                            wait(kv_full + 8 * st, par);
+                            if (!ok) break;
+                            qk(t, 0, st);
+                            release(kv_empty + 8 * st);
+                            if (j + t + 3 == n) release(q_empty);
+                            advance();
+                        }
+                    }
+                }
+                continue;
+            }
+            // The stages of tile 0's last K and tile 1's last V are released by their
+            // softmax warps when the output is written: it passes through them.
             wait(kv_full + 8 * st, par);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -475,72 +678,37 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 wait(q_full + 8 * t, qpar[t]);
                 qpar[t] ^= 1;
                 if (!ok) break;
-                qk(t, st);
+                qk(t, t, st);
                 if ((t ? n1 : n0) == 1) release(q_empty + 8 * t);
             }
             if (!ok) break;
-            release(kv_empty + 8 * st);
+            if (!whole || n0 != 1) release(kv_empty + 8 * st);
             advance();
             for (int j = 0; j < n && ok; ++j) {
                 const int sv = st;
                 wait(kv_full + 8 * sv, par);
+                if (!ok) break;
                 advance();
-                const uint32_t va = ring + static_cast<uint32_t>(sv) * C::kTile;
-                // keys of this tile; rows of V past the last one (another sequence's)
-                // could hold NaN, which a weight of zero does not undo: the MMAs stop
-                // at the next 16 keys, and the rows up to there are cleared
                 const int keys = min(128, tail - j * 128);
-                const int vsteps = (keys + 15) >> 4;
-                if (ok && (keys & 15)) {
-                    const int pad = vsteps * 16 - keys;
-                    for (int c = lane; c < pad * 8 * DA; c += 32) {
-                        const int row = keys + (c >> 3) % pad, box = (c >> 3) / pad;
-                        sts128(va + box * kABoxBytes + row * 128 + (c & 7) * 16, make_uint4(0, 0, 0, 0));
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint64_t dv = a_desc_v(va);
+                clear_tail(sv, keys);
                 bool next = false;                       // the next K tile has been waited for
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int mine = t ? n1 : n0;
-                    if (j < mine) {
-                        const uint32_t ts = tmem + 128 * t, to = tmem + 256 + 128 * t;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            wait(p_ready + 16 * t + 8 * h, ppar[t]);
-                            if (!ok) break;
-                            const uint32_t acc = j > 0 || h > 0;
-                            if (leader) {
-                                if (vsteps == 8) {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k)
-                                        a_mma_ts(to, ts + 32 * h + 8 * k, dv + 512 * h + 128 * k, id_pv,
-                                                 k > 0 ? 1u : acc);
-                                } else {
-                                    for (int k = 0; k < 4 && 4 * h + k < vsteps; ++k)
-                                        a_mma_ts(to, ts + 32 * h + 8 * k, dv + 512 * h + 128 * k, id_pv,
-                                                 k > 0 ? 1u : acc);
-                                }
-                                if (h == 1 && j == mine - 1) g_commit(o_full + 8 * t);
-                            }
-                            __syncwarp();
-                        }
-                        ppar[t] ^= 1;
-                    }
-                    if (t == 1) release(kv_empty + 8 * sv);
+                    if (j < mine) pv(t, sv, keys, j > 0, j == mine - 1);
+                    if (!ok) break;
+                    if (t == 1 && (!whole || j != n1 - 1)) release(kv_empty + 8 * sv);
                     if (j + 1 < mine) {
                         if (!next) wait(kv_full + 8 * st, par);
                         next = true;
                         if (!ok) break;
-                        qk(t, st);
+                        qk(t, t, st);
                         if (j + 2 == mine) release(q_empty + 8 * t);
                     }
                 }
-                if (j + 1 < n) {
+                if (j + 1 < n && ok) {
                     if (!next) wait(kv_full + 8 * st, par);
-                    release(kv_empty + 8 * st);
+                    if (!whole || j + 2 != n0) release(kv_empty + 8 * st);
                     advance();
                 }
             }
@@ -555,23 +723,30 @@ __global__ void __launch_bounds__(kAThreads, 1)
         regs_inc();
         const int t = warp >> 2, qtr = warp & 3;
         const int r = qtr * 32 + lane;                   // row of the tile
-        const int rt = r / g.gp, rh = r - rt * g.gp;     // its token and head in the tile
+        const int rt = r / g.gp;                         // its token in the tile
         const uint32_t lanes = static_cast<uint32_t>(qtr * 32) << 16;
         const uint32_t ts = tmem + lanes + 128 * t, to = tmem + lanes + 256 + 128 * t;
         const uint32_t sbar = s_full + 8 * t, pbar = p_ready + 16 * t, obar = o_full + 8 * t;
         int sn = 0, on = 0;                              // scores and outputs consumed
+        int kbase = 0;                                   // ring position, over the segments
         bool ok = true;
-        Segment s;
-        for (int i = 0; ok && take(i, s); ++i) {
-            if (s.t0 + t * g.tpt >= s.qlen) continue;    // no tokens in this tile
-            const int n = tiles_of(s, t);
-            const int tok = s.t0 + t * g.tpt + rt;
+        for (int i = 0; ok && take(i); give_back(i), ++i) {
+            // read from shared memory where it is needed: registers are scarce
+            const Segment &s = segs[i & 1];
+            const int n0 = tiles_of(g, s, 0), n1 = tiles_of(g, s, 1), n = t ? n1 : n0;
+            // the stage through which the output leaves (see below)
+            const int stage = (kbase + 2 * (n - 1) + t + C::kStages) % C::kStages;
+            kbase = (kbase + 2 * (g.alt ? n0 + n1 : max(n0, n1))) % C::kStages;
+            const int first = s.t0 + (g.alt ? 0 : t * g.tpt);
+            if (first >= s.qlen) continue;               // no tokens in this tile
+            // keys this row sees, from the warpgroup's first key tile on
+            const int tok = first + rt;
             const bool real = rt < g.tpt && tok < s.qlen;
-            // keys this row sees
             int lim = real ? (g.causal ? min(s.klen, tok + 1 + s.klen - s.qlen) : s.klen) : 0;
-            lim -= s.j0 * 128;
+            lim -= (s.j0 + (g.alt ? t : 0)) * 128;
+            const int step = g.alt ? 256 : 128;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < n; ++j, lim -= 128, ++sn) {
+            for (int j = 0; j < n; ++j, lim -= step, ++sn) {
                 ok = __all_sync(0xffffffffu, mbar_wait(sbar, static_cast<uint32_t>(sn & 1)));
                 if (!ok) break;
                 g_fence_after();
@@ -634,14 +809,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
                     m = mn;
                     l *= f;
                     if (j > 0) {
-                        for (int c = 0; c < g.d; c += 32) {
-                            uint32_t o[32];
-                            a_ld32(to + c, o);
-                            a_wait_ld(o);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            a_st32(to + c, o);
-                        }
+#pragma unroll 1
+                        for (int c = 0; c < g.d; c += 8) scale8(to + c, f);
                     }
                     weights(0);
                 }
@@ -662,41 +831,55 @@ __global__ void __launch_bounds__(kAThreads, 1)
             const float inv = l > 0.f || l != l ? 1.0f / l : 0.f;
             const float lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             const int64_t row = s.q0 + tok;
-            const int head = s.unit * g.gp + rh;
-            // rows of the output start on 32 bytes (the workspace's always do)
-            const bool wide = ((reinterpret_cast<uintptr_t>(g.out) & 31) | ((g.out_token | g.out_head) & 15)) == 0;
-            uint8_t *dst;
-            if (s.slot < 0) {
-                dst = static_cast<uint8_t *>(g.out) + (row * g.out_token + head * g.out_head) * 2;
-                if (real && g.lse != nullptr) g.lse[row * g.heads + head] = lse;
-            } else {
+            const int head = s.unit * g.gp + r - rt * g.gp;
+            if (s.slot >= 0) {
                 const int64_t pr = static_cast<int64_t>(s.slot) * kASlotRows + t * 128 + r;
-                dst = reinterpret_cast<uint8_t *>(g.part + pr * g.d);
+                uint8_t *dst = reinterpret_cast<uint8_t *>(g.part + pr * g.d);
                 if (real) g.part_lse[pr] = lse;
+                for (int c = 0; c < g.d; c += 32) {
+                    uint32_t o[32];
+                    load_o(o, to + c, n, inv);
+                    if (real) store_row(dst + c * 4, o, (g.d - c) * 4);
+                }
+                g_fence_before();
+                continue;
             }
+            if (real && g.lse != nullptr) g.lse[row * g.heads + head] = lse;
+            const int64_t at = (row * g.out_token + head * g.out_head) * 2;
+            const int cpr = g.d >> 3;                    // 16-byte chunks of a row
+            if (n == 0) {
+                if (real)
+                    for (int c = 0; c < cpr; ++c)
+                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(g.out) + at + 16 * c) = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            // Through shared memory, so that a store instruction writes whole rows
+            // and not 16 bytes of each of 32: the stage of the tile's last K (tile
+            // 0; every product with it is done) or V (tile 1), 32 rows a warp.
+            const uint32_t box = ring + static_cast<uint32_t>(stage) * C::kTile + qtr * 32 * DA * 128;
+            const uint32_t mine = box + lane * DA * 128;
             for (int c = 0; c < g.d; c += 32) {
                 uint32_t o[32];
-                if (n > 0) {
-                    a_ld32(to + c, o);
-                    a_wait_ld(o);
-                } else {
+                load_o(o, to + c, n, inv);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0;
-                }
-                if (!real) continue;
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    o[k] = __float_as_uint(inv == 0.f ? 0.f : __uint_as_float(o[k]) * inv);
-                if (s.slot < 0) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        o[k] = pack16(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]), F16);
-                    store_row<16>(dst + c * 2, o, (g.d - c) * 2, wide);
-                } else {
-                    store_row<32>(dst + c * 4, o, (g.d - c) * 4, true);
-                }
+                for (int k = 0; k < 4; ++k)
+                    sts128(mine + ((((c >> 3) + k) ^ (lane & 7)) << 4),
+                           make_uint4(pack16(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1]), F16),
+                                      pack16(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3]), F16),
+                                      pack16(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5]), F16),
+                                      pack16(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]), F16)));
             }
             g_fence_before();
+            __syncwarp();
+            for (int c = lane; c < 32 * cpr; c += 32) {  // 32 rows of cpr chunks, in order
+                const int rr = c / cpr, cc = c - rr * cpr;
+                const int64_t to_row = __shfl_sync(0xffffffffu, real ? at : int64_t(-1), rr);
+                const uint4 v = lds128(box + rr * DA * 128 + ((cc ^ (rr & 7)) << 4));
+                if (to_row >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(g.out) + to_row + 16 * cc) = v;
+            }
+            fence_proxy_async_smem();
+            named_barrier(1 + t, 128);
+            if (r == 0) mbar_arrive(kv_empty + 8 * stage);
         }
     }
     g_fence_before();
@@ -709,61 +892,64 @@ __global__ void __launch_bounds__(kAThreads, 1)
     }
 }
 
-// Joins the parts of the items that the split schedule cut: one warp per query
+// Joins the parts of the items that the split schedules cut: one warp per query
 // row and head.  out = sum_i w_i O_i / sum_i w_i with w_i = exp(lse_i - max lse),
-// over the parts in the order of their keys.
+// over the parts in a fixed order.
 template <bool F16>
 __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g, int grid)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t id = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    const int64_t id = blockIdx.x * int64_t(8) + (threadIdx.x >> 5);
     const int row = static_cast<int>(id / g.heads), head = static_cast<int>(id % g.heads);
     grid_dependency_wait();
     if (row >= g.tq) return;
-    // the row's item, as the schedule counts: total work, and the item's first unit
-    Cursor cur;
-    int64_t u0 = -1;
+    // the row's item, as the schedule counts: all tiles, and the item's first one
+    TileCursor cur;
+    int64_t u0 = -1, item = 0;
     int nt = 0, r = 0;
     while (cur.next(g)) {
-        const uint32_t hit = __ballot_sync(0xffffffffu, row >= cur.q0 && row < cur.q0 + cur.qlen);
+        const uint32_t hit = __ballot_sync(0xffffffffu, row >= cur.seq.q0 && row < cur.seq.q0 + cur.seq.qlen);
         if (hit != 0 && u0 < 0) {
             const int src = __ffs(hit) - 1;
-            const int tok = row - __shfl_sync(0xffffffffu, cur.q0, src);
-            const int np = __shfl_sync(0xffffffffu, cur.pairs(g), src);
-            nt = __shfl_sync(0xffffffffu, cur.tiles(g), src);
-            const int64_t first = cur.base + __shfl_sync(0xffffffffu, cur.incl, src) -
-                                  static_cast<int64_t>(np) * g.units * nt;
-            const int pair = tok / (2 * g.tpt), in = tok - pair * 2 * g.tpt;
-            u0 = first + (static_cast<int64_t>(np - 1 - pair) * g.units + head / g.gp) * nt;
+            const int tok = row - __shfl_sync(0xffffffffu, cur.seq.q0, src);
+            const int np = __shfl_sync(0xffffffffu, cur.seq.spans(g), src);
+            nt = __shfl_sync(0xffffffffu, cur.tiles(), src);
+            const int64_t items = static_cast<int64_t>(np) * g.units;
+            const int span = tok / g.span, in = tok - span * g.span;
+            const int64_t of = static_cast<int64_t>(span) * g.units + head / g.gp;
+            u0 = cur.base + __shfl_sync(0xffffffffu, cur.incl, src) - (items - of) * nt;
+            item = cur.ibase + __shfl_sync(0xffffffffu, cur.iincl, src) - items + of;
             r = in / g.tpt * 128 + in % g.tpt * g.gp + head % g.gp;
         }
     }
     if (u0 < 0) return;                                  // a row of no sequence
     const int64_t quota = (cur.base + grid - 1) / grid;
-    const int64_t c0 = u0 / quota, c1 = (u0 + nt - 1) / quota;
-    if (c0 == c1) return;                                // written whole
-    auto slot_row = [&](int64_t c) {
-        const int64_t slot = 2 * c + (c == c0 && u0 != c0 * quota ? 1 : 0);
-        return slot * kASlotRows + r;
+    const int c0 = static_cast<int>(u0 / quota), c1 = static_cast<int>((u0 + nt - 1) / quota);
+    if (c0 == c1 && !g.alt) return;                      // written whole
+    if (item + c1 >= g.slots) return;                    // only if the offsets fall
+    // part i: of CTA c0 + i, or (alt) of the warpgroups of CTA c0 + i / 2
+    const int parts = (c1 - c0 + 1) << g.alt;
+    auto part_row = [&](int i) {
+        return (item + c0 + (i >> g.alt)) * kASlotRows + r + (g.alt ? 128 * (i & 1) : 0);
     };
     float top = -INFINITY;
-    for (int64_t c = c0 + lane; c <= c1; c += 32) top = fmaxf(top, g.part_lse[slot_row(c)]);
+    for (int i = lane; i < parts; i += 32) top = fmaxf(top, g.part_lse[part_row(i)]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float ref = top == -INFINITY ? 0.f : top;
     float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
     const int col = 4 * lane;                            // d <= 128: four channels a lane
-    for (int64_t c = c0; c <= c1; ++c) {
-        const int64_t pr = slot_row(c);
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const int64_t pr = part_row(i);
         const float w = ex2_approx((g.part_lse[pr] - ref) * kLog2e);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (col < g.d) o = *reinterpret_cast<const float4 *>(g.part + pr * g.d + col);
         sum += w;
-        if (col < g.d && w != 0.f) {
-            const float4 o = *reinterpret_cast<const float4 *>(g.part + pr * g.d + col);
-            acc[0] = fmaf(w, o.x, acc[0]);
-            acc[1] = fmaf(w, o.y, acc[1]);
-            acc[2] = fmaf(w, o.z, acc[2]);
-            acc[3] = fmaf(w, o.w, acc[3]);
-        }
+        acc[0] = fmaf(w, o.x, acc[0]);
+        acc[1] = fmaf(w, o.y, acc[1]);
+        acc[2] = fmaf(w, o.z, acc[2]);
+        acc[3] = fmaf(w, o.w, acc[3]);
     }
     const float inv = sum > 0.f || sum != sum ? 1.0f / sum : 0.f;
     if (col < g.d)
@@ -802,25 +988,38 @@ int heads_per_tile(int group)
 
 constexpr int kAMaxGrid = 152;
 
-// Upper bound of the items: every sequence has at most one partly filled pair.
-int64_t items_most(int64_t tq, int64_t nseq, int64_t max_q, int64_t pair, int64_t units)
+// Upper bound of the items of `span` tokens: a sequence has at most one partly
+// filled one.
+int64_t items_most(int64_t tq, int64_t nseq, int64_t span, int64_t units)
 {
-    const int64_t by_rows = std::min(tq, tq / pair + nseq);
-    return units * std::max<int64_t>(1, std::min(by_rows, nseq * ((max_q + pair - 1) / pair)));
+    return units * std::max<int64_t>(1, std::min(tq, tq / span + nseq));
 }
 
-bool split_schedule(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_q)
-{
-    const int gp = heads_per_tile(static_cast<int>(heads / kv_heads));
-    return items_most(tq, nseq, max_q, 2 * (128 / gp), heads / gp) < kAMaxGrid;
-}
+// Fewer items than SMs: shares of key tiles (split); fewer single tiles than SMs:
+// alternate key tiles as well (alt).  Parts are numbered below items + CTAs.
+struct Schedule {
+    int gp, tpt, units;
+    bool split, alt;
+    int64_t items;
+    Schedule(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads)
+    {
+        gp = heads_per_tile(static_cast<int>(heads / kv_heads));
+        tpt = 128 / gp;
+        units = static_cast<int>(heads / gp);
+        const int64_t tiles = items_most(tq, nseq, tpt, units);
+        alt = tiles < kAMaxGrid;
+        items = alt ? tiles : items_most(tq, nseq, 2 * tpt, units);
+        split = items < kAMaxGrid;
+    }
+    int64_t slots() const { return split ? items + kAMaxGrid : 0; }
+};
 
 }  // namespace
 
-size_t attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_q)
+size_t attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d)
 {
-    if (!split_schedule(tq, nseq, heads, kv_heads, max_q)) return 0;
-    return static_cast<size_t>(kAMaxGrid) * 2 * kASlotRows * (static_cast<size_t>(d) + 1) * sizeof(float);
+    const Schedule sch(tq, nseq, heads, kv_heads);
+    return static_cast<size_t>(sch.slots()) * kASlotRows * (static_cast<size_t>(d) + 1) * sizeof(float);
 }
 
 kq_status launch_attention(const AttentionCall &c, cudaStream_t stream)
@@ -828,6 +1027,7 @@ kq_status launch_attention(const AttentionCall &c, cudaStream_t stream)
     DeviceInfo info;
     kq_status st = device_info(info);
     if (st != KQ_OK) return st;
+    const Schedule sch(c.tq, c.nseq, c.heads, c.kv_heads);
     AttnArgs g{};
     g.cu_q = c.cu_q;
     g.cu_k = c.cu_k;
@@ -836,19 +1036,22 @@ kq_status launch_attention(const AttentionCall &c, cudaStream_t stream)
     g.tk = static_cast<int>(c.tk);
     g.heads = static_cast<int>(c.heads);
     g.group = static_cast<int>(c.heads / c.kv_heads);
-    g.gp = heads_per_tile(g.group);
-    g.tpt = 128 / g.gp;
-    g.units = g.heads / g.gp;
+    g.gp = sch.gp;
+    g.tpt = sch.tpt;
+    g.units = sch.units;
     g.d = static_cast<int>(c.d);
     g.causal = c.causal ? 1 : 0;
-    g.split = split_schedule(c.tq, c.nseq, c.heads, c.kv_heads, c.max_q) ? 1 : 0;
+    g.split = sch.split ? 1 : 0;
+    g.alt = sch.alt ? 1 : 0;
+    g.span = sch.alt ? sch.tpt : 2 * sch.tpt;
     g.scale_log2 = c.scale * 1.4426950408889634f;
     g.out = c.out;
     g.out_token = c.out_token;
     g.out_head = c.out_head;
     g.lse = c.lse;
     g.part = static_cast<float *>(c.workspace);
-    g.part_lse = g.part + static_cast<int64_t>(kAMaxGrid) * 2 * kASlotRows * g.d;
+    g.slots = static_cast<int>(sch.slots());
+    g.part_lse = g.part + sch.slots() * kASlotRows * g.d;
     CUtensorMap mq, mk, mv;
     st = make_tensor_map_3d_16(&mq, c.q, c.d, c.heads, c.tq, c.q_head, c.q_token, 64,
                                static_cast<uint32_t>(g.gp), static_cast<uint32_t>(g.tpt));
@@ -861,8 +1064,7 @@ kq_status launch_attention(const AttentionCall &c, cudaStream_t stream)
         st = make_tensor_map_3d_16(&mv, vp, c.d, c.kv_heads, tk, c.v_head, c.v_token, 64, 1, 128);
     if (st != KQ_OK) return st;
     const int sms = std::min(info.sm_count, kAMaxGrid);
-    const int64_t items = items_most(c.tq, c.nseq, c.max_q, 2 * g.tpt, g.units);
-    const int grid = g.split ? sms : static_cast<int>(std::min<int64_t>(items, sms));
+    const int grid = g.split ? sms : static_cast<int>(std::min<int64_t>(sch.items, sms));
     if (c.d <= 64)
         return c.f16 ? launch_t<1, true>(mq, mk, mv, g, grid, stream)
                      : launch_t<1, false>(mq, mk, mv, g, grid, stream);

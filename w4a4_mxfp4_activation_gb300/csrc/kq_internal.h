@@ -176,7 +176,7 @@ struct AttentionCall {
     int64_t q_token, q_head, k_token, k_head, v_token, v_head;
     bool f16;
     const int32_t *cu_q, *cu_k;
-    int64_t nseq, tq, tk, heads, kv_heads, d, max_q;
+    int64_t nseq, tq, tk, heads, kv_heads, d;
     bool causal;
     float scale;
     void *out;
@@ -184,7 +184,7 @@ struct AttentionCall {
     float *lse;
     void *workspace;
 };
-size_t attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_q);
+size_t attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d);
 kq_status launch_attention(const AttentionCall &c, cudaStream_t stream);
 
 kq_status validate_quant_args(const uint16_t *A, int64_t m, int64_t d, int64_t lda,

@@ -135,9 +135,9 @@ def lib() -> ctypes.CDLL:
                                     vp]
             L.kq_linear.restype = st
             L.kq_attention.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, st, vp, vp, i64, i64,
-                                       i64, i64, i64, i64, i64, st, f32, vp, i64, i64, vp, vp, vp]
+                                       i64, i64, i64, i64, st, f32, vp, i64, i64, vp, vp, vp]
             L.kq_attention.restype = st
-            L.kq_attention_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
+            L.kq_attention_bytes.argtypes = [i64, i64, i64, i64, i64]
             L.kq_attention_bytes.restype = ctypes.c_size_t
             _lib = L
     return _lib
@@ -622,13 +622,13 @@ def _offsets(t, what: str):
     return t.numel() - 1
 
 
-def kq_attention(q, k, v, cu_q, cu_k, max_q: int, max_k: int | None = None, causal: bool = True,
+def kq_attention(q, k, v, cu_q, cu_k, max_q: int | None = None, max_k: int | None = None, causal: bool = True,
                  scale: float | None = None, lse: bool = False, out=None, stream=None):
     """Attention over packed sequences: q [tq, heads, d], k and v [tk, kv_heads,
     d] (bfloat16 or float16, any strides that are multiples of 8 elements),
     sequence b in rows cu_q[b]..cu_q[b + 1] of q and cu_k[b]..cu_k[b + 1] of k and
-    v (int32 [nseq + 1]).  max_q bounds the query lengths (``max_k`` is not
-    needed); scale defaults to 1 / sqrt(d).  Returns out [tq, heads, d], or (out,
+    v (int32 [nseq + 1]).  The bounds of the lengths, max_q and max_k, that callers
+    often carry along are not needed and not used; scale defaults to 1 / sqrt(d).  Returns out [tq, heads, d], or (out,
     lse [tq, heads] fp32) with ``lse=True``."""
     import torch
     tq, heads, d = q.shape
@@ -646,11 +646,11 @@ def kq_attention(q, k, v, cu_q, cu_k, max_q: int, max_k: int | None = None, caus
         raise ValueError("out must have the shape and type of q")
     stats = torch.empty((tq, heads), dtype=torch.float32, device=q.device) if lse else None
     L = lib()
-    nbytes = L.kq_attention_bytes(tq, nseq, heads, kv_heads, d, max_q)
+    nbytes = L.kq_attention_bytes(tq, nseq, heads, kv_heads, d)
     work = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
     _check(L.kq_attention(_ptr(q), *_heads(q, "q"), _ptr(k), *_heads(k, "k"), _ptr(v),
                           *_heads(v, "v"), _format(q.dtype), _ptr(cu_q), _ptr(cu_k), nseq, tq, tk,
-                          heads, kv_heads, d, max_q, 1 if causal else 0,
+                          heads, kv_heads, d, 1 if causal else 0,
                           d ** -0.5 if scale is None else scale, _ptr(out), *_heads(out, "out"),
                           _ptr(stats), _ptr(work), _stream(stream)),
            "kq_attention")
