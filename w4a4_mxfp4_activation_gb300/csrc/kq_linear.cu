@@ -12,6 +12,7 @@
 // TMEM lane each) and the tokens the N side (16 to 128), so a token costs one
 // accumulator column and not one of 128 padded rows.
 #include <algorithm>
+#include <mutex>
 
 #include "kq_device.cuh"
 #include "kq_epilogue.cuh"
@@ -22,7 +23,8 @@ namespace kq {
 namespace {
 
 constexpr int kSWBytes = 128 * 128;                 // W per stage: 128 rows x 128 bytes
-constexpr int kSThreads = 192;                      // producer, MMA, 4 epilogue warps
+constexpr int kSThreads = 192;                      // warp 1 MMAs, warps 2-5 read the accumulator
+constexpr int kSProducers = 5;                      // warps 0, 2-5 issue the loads
 constexpr int kSMaxStages = 8;
 constexpr int kSBarBytes = 256;
 constexpr int kSRingBytes = 200 * 1024;
@@ -107,13 +109,34 @@ __global__ void __launch_bounds__(kSThreads, 1)
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(tmem_slot) : "memory");
     grid_dependency_wait();
 
+    // a thread's first four elements of the join below, and their bias and residual,
+    // which are fetched while the product runs
+    const int rows = static_cast<int>(min(int64_t(g.tokens), g.m - mt * g.tokens));
+    const int units = rows * 32;
+    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / g.splits);
+    int u = static_cast<int>(static_cast<int64_t>(units) * rank / g.splits) + threadIdx.x;
+    float side_b[4], side_r[4];
+    auto fetch = [&] {
+        const int64_t row = mt * g.tokens + (u >> 5), col = nt * 128 + 4 * (u & 31);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            side_b[j] = side_r[j] = 0.f;
+            if (u < u1 && col + j < g.n) {
+                if (g.bias != nullptr) side_b[j] = __ldg(g.bias + col + j);
+                if (g.residual != nullptr) side_r[j] = load_residual(g.residual, row * g.ldr + col + j, g.fmt);
+            }
+        }
+    };
+
     bool ok = true;
-    if (warp == 0) {
+    if (warp != 1) {
+        // Issuing a stage's copies takes one thread 450 to 600 cycles, as long as
+        // HBM takes for the bytes: five warps take every fifth stage each.
         if (lane == 0) {
-            int s = 0, issued = 0;
-            uint32_t par = 1;                        // the first round needs no wait
-            for (int ks = k0; ks < k1; ++ks) {
-                if (ks - k0 >= g.stages && !mbar_wait(empty + 8 * s, par)) break;
+            const int me = warp == 0 ? 0 : warp - 1;
+            for (int i = me; i < k1 - k0; i += kSProducers) {
+                const int s = i % g.stages, round = i / g.stages, ks = k0 + i;
+                if (round > 0 && !mbar_wait(empty + 8 * s, static_cast<uint32_t>((round - 1) & 1))) break;
                 const uint32_t st = base + static_cast<uint32_t>(s) * stage_bytes, fb = full + 8 * s;
                 uint32_t sf_bytes = 0;
                 if constexpr (MX) {
@@ -129,17 +152,10 @@ __global__ void __launch_bounds__(kSThreads, 1)
                     bulk_load(st + sfw_off, g.sfw + (nt * g.ncb + 2 * ks) * 512, sf_bytes, fb);
                     bulk_load(st + sfx_off, g.sfa + (mt * g.ncb + 2 * ks) * 512, sf_bytes, fb);
                 }
-                ++issued;
-                if (++s == g.stages) {
-                    s = 0;
-                    par ^= 1;
-                }
             }
-            // the last copies have landed before the ring is reused or left
-            for (int j = max(0, issued - g.stages); j < issued; ++j)
-                (void)mbar_wait(full + 8 * (j % g.stages), static_cast<uint32_t>((j / g.stages) & 1));
         }
         __syncwarp();
+        fetch();
     } else if (warp == 1) {
         const bool leader = elect_one();
         const bool pad_fix = MX && (g.nb & 1) != 0;
@@ -201,9 +217,15 @@ __global__ void __launch_bounds__(kSThreads, 1)
         }
     }
     // all warps: the accumulator is complete, and the ring free for the parts
+    // (the products have read every copy)
     ok = mbar_wait(done, 0, 2 * kWaitLimitNs) && ok;
-    __syncthreads();                                 // the producer's copies have landed too
-    const int rows = static_cast<int>(min(int64_t(g.tokens), g.m - mt * g.tokens));
+    if (!ok && threadIdx.x == 0) {
+        // a wait gave up: the last copy into each stage, if there was one, has landed
+        // before the ring is reused or left
+        for (int i = max(0, k1 - k0 - g.stages); i < k1 - k0; ++i)
+            (void)mbar_wait(full + 8 * (i % g.stages), static_cast<uint32_t>((i / g.stages) & 1));
+    }
+    __syncthreads();
     if (warp >= 2) {
         // part[token][weight row] in fp32; a part that is not there is NaN
         const int q = warp & 3;
@@ -224,11 +246,9 @@ __global__ void __launch_bounds__(kSThreads, 1)
     cluster_wait();
     // the tile's elements, four neighbouring channels a thread, spread over the
     // cluster; every sum runs over the ranks in order
-    const int units = rows * 32;
-    const int u1 = static_cast<int>(static_cast<int64_t>(units) * (rank + 1) / g.splits);
     const bool f16 = g.fmt == KQ_F16;
-    for (int u = static_cast<int>(static_cast<int64_t>(units) * rank / g.splits) + threadIdx.x; u < u1;
-         u += kSThreads) {
+    if (warp == 1) fetch();
+    for (; u < u1; u += kSThreads, fetch()) {
         const int64_t row = mt * g.tokens + (u >> 5), col = nt * 128 + 4 * (u & 31);
         if (col >= g.n) continue;
         const uint32_t at = base + static_cast<uint32_t>(u) * 16u;
@@ -246,17 +266,13 @@ __global__ void __launch_bounds__(kSThreads, 1)
                 v[3] += p[r].w;
             }
         }
-        const int left = static_cast<int>(min(int64_t(4), g.n - col));
-        if (g.bias != nullptr)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < left) v[j] += __ldg(g.bias + col + j);
+        for (int j = 0; j < 4; ++j) v[j] += side_b[j];
         apply_act(v, g.act);
-        if (g.residual != nullptr)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < left) v[j] += load_residual(g.residual, row * g.ldr + col + j, g.fmt);
+        for (int j = 0; j < 4; ++j) v[j] += side_r[j];
         const int64_t o = row * g.ldo + col;
+        const int left = static_cast<int>(min(int64_t(4), g.n - col));
         if (left == 4 && g.fmt != KQ_F32) {
             *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(g.out) + o) =
                 make_uint2(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16));
@@ -278,31 +294,59 @@ __global__ void __launch_bounds__(kSThreads, 1)
 }
 
 template <bool MX>
+struct SplitLaunch {
+    static constexpr int kSmem = kSRingBytes + kSBarBytes + 1024;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    SplitLaunch(int64_t ctas, int splits, cudaStream_t stream)
+    {
+        cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+        cfg.blockDim = dim3(kSThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
+
+// Sets the kernel up, once per device, and gives the clusters of each size that are
+// resident at once: a cluster lives within one group of SMs, so 152 SMs hold fewer
+// than 152 / size (24 clusters of 6 took two rounds: 14.6 us against 7.3).
+template <bool MX>
+kq_status split_residency(int (&clusters)[kSMaxSplit + 1])
+{
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    static int most[64][kSMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KQ_ERR_CUDA;
+    std::call_once(once[dev], [dev] {
+        auto kern = split_kernel<MX>;
+        err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        SplitLaunch<MX>::kSmem);
+        for (int n = 2; n <= kSMaxSplit && err[dev] == cudaSuccess; ++n) {
+            SplitLaunch<MX> l(n, n, nullptr);
+            l.cfg.numAttrs = 1;
+            err[dev] = cudaOccupancyMaxActiveClusters(&most[dev][n], kern, &l.cfg);
+        }
+    });
+    if (err[dev] != cudaSuccess) return KQ_ERR_CUDA;
+    std::copy(most[dev], most[dev] + kSMaxSplit + 1, clusters);
+    return KQ_OK;
+}
+
+template <bool MX>
 kq_status launch_split(const CUtensorMap &mx, const CUtensorMap &mw, const SplitArgs &g,
                        int64_t tiles, cudaStream_t stream)
 {
-    constexpr int kSmem = kSRingBytes + kSBarBytes + 1024;
-    auto kern = split_kernel<MX>;
-    static DeviceOnce once;
-    const kq_status st = once.run([&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    });
-    if (st != KQ_OK) return st;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * g.splits));
-    cfg.blockDim = dim3(kSThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(g.splits);
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, mx, mw, g) == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
+    SplitLaunch<MX> l(tiles * g.splits, g.splits, stream);
+    return cudaLaunchKernelEx(&l.cfg, split_kernel<MX>, mx, mw, g) == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
 }
 
 }  // namespace
@@ -314,7 +358,13 @@ kq_status launch_linear(const LinearCall &c, cudaStream_t stream)
     if (st != KQ_OK) return st;
     const int64_t ntiles = (c.n + 127) / 128, mtiles = (c.m + 127) / 128, tiles = mtiles * ntiles;
     const int64_t ksteps = (c.k + (c.mx ? 255 : 63)) / (c.mx ? 256 : 64);
-    const int64_t splits = std::min<int64_t>({kSMaxSplit, info.sm_count / tiles, ksteps});
+    if (2 * tiles > info.sm_count || ksteps < 2) return launch_linear_tiles(c, stream);
+    int clusters[kSMaxSplit + 1];
+    st = c.mx ? split_residency<true>(clusters) : split_residency<false>(clusters);
+    if (st != KQ_OK) return st;
+    // the most parts with which all tiles run at once
+    int splits = static_cast<int>(std::min<int64_t>(kSMaxSplit, ksteps));
+    while (splits > 1 && clusters[splits] < tiles) --splits;
     if (splits < 2) return launch_linear_tiles(c, stream);
 
     SplitArgs g{};
@@ -328,7 +378,7 @@ kq_status launch_linear(const LinearCall &c, cudaStream_t stream)
     g.ntiles = ntiles;
     g.ksteps = static_cast<int>(ksteps);
     g.tokens = c.m >= 128 ? 128 : static_cast<int>((c.m + 15) / 16 * 16);
-    g.splits = static_cast<int>(splits);
+    g.splits = splits;
     const int stage = kSWBytes + g.tokens * 128 + (c.mx ? 2048 : 0);
     g.stages = std::min(kSMaxStages, kSRingBytes / stage);
     g.f16 = !c.mx && c.fmt_in == KQ_F16;

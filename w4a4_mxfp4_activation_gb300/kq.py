@@ -444,51 +444,72 @@ def kq_layer_error(c, c_ref, out=None, stream=None):
 
 
 # --- the operators of a transformer block around the quantizer ---------------------
+#
+# A call on one token takes the GPU a few microseconds, so what happens here counts:
+# each check and each lookup is made once.
 
-_FORMAT = None
+_FORMAT = {}                # torch dtype -> kq_format, filled with the first use of torch
+_torch = None
+_raw_stream = None
+
+
+def _load_torch():
+    """torch, and its function for the current stream's handle (without a Stream
+    object around it)."""
+    global _torch, _raw_stream
+    import torch
+    _FORMAT.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+        (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _handle(stream, device):
+    """The handle of ``stream``, or of the current stream of ``device``."""
+    if stream is not None:
+        return stream.cuda_stream
+    if device.type != "cuda":
+        raise ValueError("CUDA tensors expected")
+    return _raw_stream(device.index)
 
 
 def _format(dtype) -> int:
     """kq_format of a torch dtype (bfloat16, float16 or float32)."""
-    global _FORMAT
-    if _FORMAT is None:
-        import torch
-        _FORMAT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
     try:
         return _FORMAT[dtype]
     except KeyError:
         raise TypeError(f"bfloat16, float16 or float32 expected, got {dtype}") from None
 
 
-def _rows(t, what: str):
-    """A [rows, columns] tensor whose columns are adjacent: its row pitch."""
-    if t.dim() != 2:
+def _rows(t, m: int, n: int, fmt: int, what: str) -> int:
+    """The row pitch of an [m, n] tensor whose columns are adjacent."""
+    st = t.stride()
+    if len(st) != 2:
         raise ValueError(f"{what} must be two-dimensional")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    if st[1] != 1 and n > 1:
         raise ValueError(f"{what}: the columns of a row must be adjacent in memory")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), _pitch(t.shape[1], t.dtype))
-
-
-def _pitch(n: int, dtype) -> int:
-    """n rounded up to a row pitch of a multiple of 16 bytes."""
-    unit = 4 if _format(dtype) == 2 else 8
+    if m > 1:
+        return st[0]
+    # the pitch of a single row (or none) is not used: one that passes the checks
+    unit = 4 if fmt == 2 else 8
     return n + (-n) % unit
 
 
-def _empty_rows(m: int, n: int, dtype, device):
-    """[m, n] of ``dtype`` with a row pitch of a multiple of 16 bytes."""
-    import torch
-    ld = _pitch(n, dtype)
-    t = torch.empty((m, ld), dtype=dtype, device=device)
-    return t if ld == n else t[:, :n]
+def _empty_rows(m: int, n: int, dtype, fmt: int, device):
+    """[m, n] of ``dtype`` with a row pitch of a multiple of 16 bytes, and the pitch."""
+    unit = 4 if fmt == 2 else 8
+    if n % unit == 0:
+        return _torch.empty((m, n), dtype=dtype, device=device), n
+    ld = n + (-n) % unit
+    return _torch.empty((m, ld), dtype=dtype, device=device)[:, :n], ld
 
 
 def _f32(t, what: str, *shape):
     """fp32, contiguous, of the given shape (or None): its pointer."""
     if t is None:
         return None
-    import torch
-    if t.dtype != torch.float32 or not t.is_contiguous():
+    if t.dtype != _torch.float32 or not t.is_contiguous():
         raise TypeError(f"{what} must be contiguous float32")
     n = 1
     for v in shape:
@@ -508,21 +529,25 @@ def kq_layer_norm(x, weight=None, bias=None, eps: float = 1e-6, group_rows: int 
     weight, bias: fp32 [groups, d] (or [d]), one row for every ``group_rows``
     rows of x (0: one for all).  Returns y, or (y, mean, rstd) with
     ``stats=True`` (fp32 [m], for the backward pass)."""
-    import torch
+    torch = _torch or _load_torch()
     m, d = x.shape
-    fmt, ldx = _format(x.dtype), _rows(x, "x")
-    groups = _groups(m, group_rows)
+    dtype, device = x.dtype, x.device
+    fmt = _format(dtype)
+    ldx = _rows(x, m, d, fmt, "x")
+    groups = 1 if group_rows == 0 else _groups(m, group_rows)
+    w, b = _f32(weight, "weight", groups, d), _f32(bias, "bias", groups, d)
     if y is None:
-        y = _empty_rows(m, d, x.dtype, x.device)
-    elif y.shape != x.shape or y.dtype != x.dtype:
+        y, ldy = _empty_rows(m, d, dtype, fmt, device)
+    elif y.shape != x.shape or y.dtype != dtype:
         raise ValueError("y must have the shape and type of x")
-    mean = rstd = None
+    else:
+        ldy = _rows(y, m, d, fmt, "y")
+    mean = rstd = pm = pr = None
     if stats:
-        mean = torch.empty(m, dtype=torch.float32, device=x.device)
-        rstd = torch.empty(m, dtype=torch.float32, device=x.device)
-    _check(lib().kq_layer_norm(_ptr(x), ldx, fmt, m, d, _f32(weight, "weight", groups, d),
-                               _f32(bias, "bias", groups, d), group_rows, eps, _ptr(y),
-                               _rows(y, "y"), _ptr(mean), _ptr(rstd), _stream(stream)),
+        mean, rstd = torch.empty((2, m), dtype=torch.float32, device=device).unbind(0)
+        pm, pr = mean.data_ptr(), rstd.data_ptr()
+    _check((_lib or lib()).kq_layer_norm(x.data_ptr(), ldx, fmt, m, d, w, b, group_rows, eps,
+                                         y.data_ptr(), ldy, pm, pr, _handle(stream, device)),
            "kq_layer_norm")
     return (y, mean, rstd) if stats else y
 
@@ -531,40 +556,47 @@ def kq_layer_norm_backward(dy, x, weight, mean, rstd, group_rows: int = 0, dx=No
                            stream=None):
     """Gradient of kq_layer_norm.  Returns (dx, dweight, dbias): dx in the
     type of x, dweight and dbias fp32 [groups, d]."""
-    import torch
+    torch = _torch or _load_torch()
     m, d = x.shape
-    fmt = _format(x.dtype)
-    if dy.shape != x.shape or dy.dtype != x.dtype:
+    dtype, device = x.dtype, x.device
+    fmt = _format(dtype)
+    if dy.shape != x.shape or dy.dtype != dtype:
         raise ValueError("dy must have the shape and type of x")
+    ldx, lddy = _rows(x, m, d, fmt, "x"), _rows(dy, m, d, fmt, "dy")
     groups = _groups(m, group_rows)
+    w = _f32(weight, "weight", groups, d)
+    pm, pr = _f32(mean, "mean", m), _f32(rstd, "rstd", m)
     if dx is None:
-        dx = _empty_rows(m, d, x.dtype, x.device)
-    elif dx.shape != x.shape or dx.dtype != x.dtype:
+        dx, lddx = _empty_rows(m, d, dtype, fmt, device)
+    elif dx.shape != x.shape or dx.dtype != dtype:
         raise ValueError("dx must have the shape and type of x")
-    grads = torch.empty((2, groups, d), dtype=torch.float32, device=x.device)
-    nbytes = int(lib().kq_layer_norm_backward_bytes(m, d, group_rows))
-    work = torch.empty(nbytes, dtype=torch.uint8, device=x.device) if nbytes else None
-    dweight, dbias = grads[0], grads[1]
-    _check(lib().kq_layer_norm_backward(_ptr(dy), _rows(dy, "dy"), _ptr(x), _rows(x, "x"), fmt, m,
-                                        d, _f32(weight, "weight", groups, d), group_rows,
-                                        _f32(mean, "mean", m), _f32(rstd, "rstd", m), _ptr(dx),
-                                        _rows(dx, "dx"), _ptr(dweight), _ptr(dbias), _ptr(work),
-                                        _stream(stream)),
+    else:
+        lddx = _rows(dx, m, d, fmt, "dx")
+    L = _lib or lib()
+    dweight, dbias = torch.empty((2, groups, d), dtype=torch.float32, device=device).unbind(0)
+    nbytes = L.kq_layer_norm_backward_bytes(m, d, group_rows)
+    work = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    _check(L.kq_layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, fmt, m, d, w,
+                                    group_rows, pm, pr, dx.data_ptr(), lddx, dweight.data_ptr(),
+                                    dbias.data_ptr(), work.data_ptr() if nbytes else None,
+                                    _handle(stream, device)),
            "kq_layer_norm_backward")
     return dx, dweight, dbias
 
 
-def _linear_out(m, n, residual, out, out_dtype, device):
-    """(out, residual pointer, residual pitch) of a linear layer."""
+def _linear_out(m, n, residual, out, out_dtype, fmt, device):
+    """(out, its pitch, residual pointer, its pitch) of a linear layer."""
     if out is None:
-        out = _empty_rows(m, n, out_dtype, device)
+        out, ldo = _empty_rows(m, n, out_dtype, fmt, device)
     elif tuple(out.shape) != (m, n) or out.dtype != out_dtype:
         raise ValueError(f"out must be [{m}, {n}] of {out_dtype}")
+    else:
+        ldo = _rows(out, m, n, fmt, "out")
     if residual is None:
-        return out, None, 0
+        return out, ldo, None, 0
     if tuple(residual.shape) != (m, n) or residual.dtype != out_dtype:
         raise ValueError(f"residual must be [{m}, {n}] of {out_dtype}")
-    return out, residual.data_ptr(), _rows(residual, "residual")
+    return out, ldo, residual.data_ptr(), _rows(residual, m, n, fmt, "residual")
 
 
 def kq_w4a4_linear(qa, sfa, qw, sfw, m: int, n: int, k: int, bias=None, act: str = "none",
@@ -572,13 +604,17 @@ def kq_w4a4_linear(qa, sfa, qw, sfw, m: int, n: int, k: int, bias=None, act: str
     """residual + act(deq(qa) deq(qw)^T + bias) as [m, n] of ``out_dtype``
     (bfloat16 when not given), from packed codes and 128x4 tiled scales.
     bias: fp32 [n]; act in KQ_ACT; residual: [m, n] of ``out_dtype``."""
+    torch = _torch or _load_torch()
     if out_dtype is None:
-        import torch
         out_dtype = torch.bfloat16 if out is None else out.dtype
-    out, res, ldr = _linear_out(m, n, residual, out, out_dtype, qa.device)
-    _check(lib().kq_w4a4_linear(_ptr(qa), _ld(qa, k // 2), _ptr(sfa), _ptr(qw), _ld(qw, k // 2),
-                                _ptr(sfw), m, n, k, _f32(bias, "bias", n), KQ_ACT[act], res, ldr,
-                                _ptr(out), _rows(out, "out"), _format(out_dtype), _stream(stream)),
+    device = qa.device
+    fmt = _format(out_dtype)
+    pb = _f32(bias, "bias", n)
+    out, ldo, res, ldr = _linear_out(m, n, residual, out, out_dtype, fmt, device)
+    _check((_lib or lib()).kq_w4a4_linear(qa.data_ptr(), _ld(qa, k // 2), sfa.data_ptr(),
+                                          qw.data_ptr(), _ld(qw, k // 2), sfw.data_ptr(), m, n, k,
+                                          pb, KQ_ACT[act], res, ldr, out.data_ptr(), ldo, fmt,
+                                          _handle(stream, device)),
            "kq_w4a4_linear")
     return out
 
@@ -588,16 +624,20 @@ def kq_linear(a, w, bias=None, act: str = "none", residual=None, out=None, out_d
     """residual + act(a w^T + bias) for a [m, k] and w [n, k], both bfloat16 or
     both float16; the result is [m, n] of ``out_dtype`` (a's type when not
     given).  bias: fp32 [n]; act in KQ_ACT; residual: [m, n] of ``out_dtype``."""
+    _torch or _load_torch()
     m, k = a.shape
-    n = w.shape[0]
-    if w.shape[1] != k or w.dtype != a.dtype:
+    n, kw = w.shape
+    dtype, device = a.dtype, a.device
+    if kw != k or w.dtype != dtype:
         raise ValueError("a and w must have the same number of columns and the same type")
     if out_dtype is None:
-        out_dtype = a.dtype if out is None else out.dtype
-    out, res, ldr = _linear_out(m, n, residual, out, out_dtype, a.device)
-    _check(lib().kq_linear(_ptr(a), _rows(a, "a"), _ptr(w), _rows(w, "w"), _format(a.dtype), m, n, k,
-                           _f32(bias, "bias", n), KQ_ACT[act], res, ldr, _ptr(out),
-                           _rows(out, "out"), _format(out_dtype), _stream(stream)),
+        out_dtype = dtype if out is None else out.dtype
+    fmt_in, fmt = _format(dtype), _format(out_dtype)
+    pb = _f32(bias, "bias", n)
+    out, ldo, res, ldr = _linear_out(m, n, residual, out, out_dtype, fmt, device)
+    _check((_lib or lib()).kq_linear(a.data_ptr(), _rows(a, m, k, fmt_in, "a"), w.data_ptr(),
+                                     _rows(w, n, k, fmt_in, "w"), fmt_in, m, n, k, pb, KQ_ACT[act],
+                                     res, ldr, out.data_ptr(), ldo, fmt, _handle(stream, device)),
            "kq_linear")
     return out
 
@@ -616,42 +656,47 @@ def _heads(t, what: str):
 
 
 def _offsets(t, what: str):
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+    if t.dtype != _torch.int32 or t.dim() != 1 or not t.is_contiguous():
         raise TypeError(f"{what} must be a contiguous one-dimensional int32 tensor")
     return t.numel() - 1
 
 
-def kq_attention(q, k, v, cu_q, cu_k, max_q: int | None = None, max_k: int | None = None, causal: bool = True,
-                 scale: float | None = None, lse: bool = False, out=None, stream=None):
+def kq_attention(q, k, v, cu_q, cu_k, max_q: int | None = None, max_k: int | None = None,
+                 causal: bool = True, scale: float | None = None, lse: bool = False, out=None,
+                 stream=None):
     """Attention over packed sequences: q [tq, heads, d], k and v [tk, kv_heads,
     d] (bfloat16 or float16, any strides that are multiples of 8 elements),
     sequence b in rows cu_q[b]..cu_q[b + 1] of q and cu_k[b]..cu_k[b + 1] of k and
     v (int32 [nseq + 1]).  The bounds of the lengths, max_q and max_k, that callers
-    often carry along are not needed and not used; scale defaults to 1 / sqrt(d).  Returns out [tq, heads, d], or (out,
-    lse [tq, heads] fp32) with ``lse=True``."""
-    import torch
+    often carry along are not needed and not used; scale defaults to 1 / sqrt(d).
+    Returns out [tq, heads, d], or (out, lse [tq, heads] fp32) with ``lse=True``."""
+    torch = _torch or _load_torch()
+    q_token, q_head = _heads(q, "q")
     tq, heads, d = q.shape
-    tk, kv_heads = k.shape[0], k.shape[1]
-    if k.shape != v.shape or k.shape[2] != d or k.dtype != q.dtype or v.dtype != q.dtype:
+    dtype, device = q.dtype, q.device
+    if k.shape != v.shape or k.dim() != 3 or k.shape[2] != d or k.dtype != dtype or v.dtype != dtype:
         raise ValueError("k and v must have one shape, and the type and last dimension of q")
+    tk, kv_heads, _ = k.shape
     nseq = _offsets(cu_q, "cu_q")
-    if _offsets(cu_k, "cu_k") != nseq:
-        raise ValueError("cu_q and cu_k must have the same number of entries")
-    if nseq < 0:
-        raise ValueError("cu_q and cu_k must have at least one entry")
+    if _offsets(cu_k, "cu_k") != nseq or nseq < 0:
+        raise ValueError("cu_q and cu_k must have the same number of entries, at least one")
+    fmt = _format(dtype)
     if out is None:
-        out = torch.empty((tq, heads, d), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+        out = torch.empty((tq, heads, d), dtype=dtype, device=device)
+        o_token, o_head = heads * d, d
+    elif out.shape != q.shape or out.dtype != dtype:
         raise ValueError("out must have the shape and type of q")
-    stats = torch.empty((tq, heads), dtype=torch.float32, device=q.device) if lse else None
-    L = lib()
+    else:
+        o_token, o_head = _heads(out, "out")
+    stats = torch.empty((tq, heads), dtype=torch.float32, device=device) if lse else None
+    L = _lib or lib()
     nbytes = L.kq_attention_bytes(tq, nseq, heads, kv_heads, d)
-    work = torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
-    _check(L.kq_attention(_ptr(q), *_heads(q, "q"), _ptr(k), *_heads(k, "k"), _ptr(v),
-                          *_heads(v, "v"), _format(q.dtype), _ptr(cu_q), _ptr(cu_k), nseq, tq, tk,
-                          heads, kv_heads, d, 1 if causal else 0,
-                          d ** -0.5 if scale is None else scale, _ptr(out), *_heads(out, "out"),
-                          _ptr(stats), _ptr(work), _stream(stream)),
+    work = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    _check(L.kq_attention(q.data_ptr(), q_token, q_head, k.data_ptr(), *_heads(k, "k"),
+                          v.data_ptr(), *_heads(v, "v"), fmt, cu_q.data_ptr(), cu_k.data_ptr(), nseq,
+                          tq, tk, heads, kv_heads, d, 1 if causal else 0,
+                          d ** -0.5 if scale is None else scale, out.data_ptr(), o_token, o_head,
+                          stats.data_ptr() if lse else None, work.data_ptr() if nbytes else None,
+                          _handle(stream, device)),
            "kq_attention")
     return (out, stats) if lse else out
