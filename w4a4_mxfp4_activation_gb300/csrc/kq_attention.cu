@@ -285,24 +285,6 @@ __device__ __forceinline__ uint64_t a_desc_v(uint32_t saddr)
            (1ull << 46) | (2ull << 61);
 }
 
-#define KQ_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), \
-                    "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
-#define KQ_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), \
-                    "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
-#define KQ_IO8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), \
-                     "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
-
-// 32 columns of the warp's lanes, complete after a_wait_ld on the registers.
-__device__ __forceinline__ void a_ld32(uint32_t taddr, uint32_t *r)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : KQ_R8(r, 0), KQ_R8(r, 8), KQ_R8(r, 16), KQ_R8(r, 24)
-        : "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ void a_st32(uint32_t taddr, const uint32_t *r)
 {
     asm volatile(
@@ -311,15 +293,6 @@ __device__ __forceinline__ void a_st32(uint32_t taddr, const uint32_t *r)
         "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
         KQ_I8(r, 0), KQ_I8(r, 8), KQ_I8(r, 16), KQ_I8(r, 24)
         : "memory");
-}
-// Waits for the loads; the registers pass through, so that no use of them can be
-// moved ahead of the wait.
-__device__ __forceinline__ void a_wait_ld(uint32_t *r)
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : KQ_IO8(r, 0), KQ_IO8(r, 8), KQ_IO8(r, 16), KQ_IO8(r, 24)
-                 :
-                 : "memory");
 }
 __device__ __forceinline__ void a_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -353,8 +326,8 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void load_o(uint32_t (&o)[32], uint32_t taddr, int n, float inv)
 {
     if (n > 0) {
-        a_ld32(taddr, o);
-        a_wait_ld(o);
+        g_ld32_issue(taddr, o);
+        g_wait_ld32(o);
     }
 #pragma unroll
     for (int k = 0; k < 32; ++k)
@@ -366,10 +339,7 @@ __device__ __forceinline__ void store_row(uint8_t *dst, const uint32_t (&o)[32],
 {
 #pragma unroll
     for (int k = 0; k < 32; k += 8)
-        if (4 * k < left)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 4 * k),
-                         KQ_I8(o, k)
-                         : "memory");
+        if (4 * k < left) stg256(dst + 4 * k, o + k);
 }
 
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kARegsOther)); }
@@ -752,9 +722,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 g_fence_after();
                 uint32_t v[128];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) a_ld32(ts + 32 * c, v + 32 * c);
+                for (int c = 0; c < 4; ++c) g_ld32_issue(ts + 32 * c, v + 32 * c);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) a_wait_ld(v + 32 * c);
+                for (int c = 0; c < 4; ++c) g_wait_ld32(v + 32 * c);
                 if (__any_sync(0xffffffffu, lim < 128)) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c)

@@ -72,6 +72,38 @@ __device__ __forceinline__ void g_ld16(uint32_t taddr, uint32_t (&r)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// The same without the wait: the registers are complete after g_wait_ld32, which
+// they pass through, so that no use of them can be moved ahead of it.
+#define KQ_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), \
+                    "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+#define KQ_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), \
+                    "r"(r[o + 5]), "r"(r[o + 6]), "r"(r[o + 7])
+#define KQ_IO8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), \
+                     "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
+__device__ __forceinline__ void g_ld32_issue(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : KQ_R8(r, 0), KQ_R8(r, 8), KQ_R8(r, 16), KQ_R8(r, 24)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void g_wait_ld32(uint32_t *r)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : KQ_IO8(r, 0), KQ_IO8(r, 8), KQ_IO8(r, 16), KQ_IO8(r, 24)
+                 :
+                 : "memory");
+}
+
+// 32 bytes to a 32-byte aligned address.
+__device__ __forceinline__ void stg256(void *p, const uint32_t *r)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), KQ_I8(r, 0) : "memory");
+}
+
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
