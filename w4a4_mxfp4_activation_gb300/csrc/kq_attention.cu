@@ -342,9 +342,6 @@ __device__ __forceinline__ void store_row(uint8_t *dst, const uint32_t (&o)[32],
         if (4 * k < left) stg256(dst + 4 * k, o + k);
 }
 
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kARegsOther)); }
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kARegsSoftmax)); }
-
 // ---- the kernel ------------------------------------------------------------------------
 
 template <int DA, bool F16>
@@ -410,7 +407,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
 
     if (warp == 8) {
         // schedule and loads
-        regs_dec();
+        regs_dec<kARegsOther>();
         LevelCursor items;
         TileCursor tiles;
         int64_t w = 0, end = 0, item = 0;
@@ -509,7 +506,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     } else if (warp == 9) {
         // MMAs: one elected lane issues, the warp waits converged.  Its operands are
         // warp-uniform and its full tiles straight-line code.
-        regs_dec();
+        regs_dec<kARegsOther>();
         const bool leader = elect_one();
         constexpr uint32_t kFmt = F16 ? 0u : ((1u << 7) | (1u << 10));
         constexpr uint32_t id_qk = (1u << 4) | kFmt | ((128u >> 3) << 17) | ((128u >> 4) << 24);
@@ -688,9 +685,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
         __syncwarp();
         (void)mbar_wait(drain, 0);
     } else if (warp >= 10) {
-        regs_dec();
+        regs_dec<kARegsOther>();
     } else {
-        regs_inc();
+        regs_inc<kARegsSoftmax>();
         const int t = warp >> 2, qtr = warp & 3;
         const int r = qtr * 32 + lane;                   // row of the tile
         const int rt = r / g.gp;                         // its token in the tile

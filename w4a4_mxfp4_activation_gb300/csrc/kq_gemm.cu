@@ -358,7 +358,9 @@ struct XCfg {
     static constexpr int kStages = 4;
     static constexpr int kEpiWarps = EPI != 0 ? 8 : 4 * NH;
     static constexpr int kEpiCols = kBN * 4 / kEpiWarps;  // columns of the tile per epilogue warp
-    static constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer, MMA, epilogue
+    // producer, MMA, epilogue; the linear layers: three warpgroups, the epilogue's
+    // first, so that registers can move to it
+    static constexpr int kThreads = EPI != 0 ? 384 : 64 + 32 * kEpiWarps;
     // the bf16 product has no scales in TMEM, so a linear layer's wide tile has
     // room for a second accumulator; the plain product releases its only one early
     static constexpr int kAccBufs = NH == 1 || (EPI != 0 && !MX) ? 2 : 1;
@@ -383,16 +385,24 @@ struct XCfg {
     static_assert(kSmemBytes <= 227 * 1024, "shared memory of one CTA");
 };
 
+// Registers of the linear layers' warps: 256 * 216 + 128 * 72 = 384 * 168, what the
+// launch gives.
+constexpr int kEpiRegs = 216, kEpiRegsOther = 72;
+
 // The linear layers' epilogue of one warp: 32 rows (one a lane) x COLS columns of
-// the tile, 32 columns at a time.  The accumulator is read in these steps, one step
-// ahead, and released after the last: the loop is not unrolled, so that three
-// activations fit the instruction cache.  Each lane fetches its row's residual a
+// the tile, 32 columns at a time.  The loop is not unrolled, so that three
+// activations fit the instruction cache.  With two accumulators, it is read in these
+// steps, one step ahead, and released after the last.  The wide MXFP4 tile has one
+// (EARLY): all columns are read into registers first and it is released before they
+// are worked on, the registers moving down by 32 from step to step (4608 x 12288 x
+// 3072: 112.6 us with the late release).  Each lane fetches its row's residual a
 // step ahead, the first one before the accumulator is ready, and stores its 64 or
 // 128 bytes of the row itself, 32 bytes an instruction.  (Boxes in shared memory and
 // TMA stores, as in the plain product, took 28.2 us on 4096 x 4608 x 1152 against
 // 19.9 for the product: a proxy fence and a store per 2 KB.)
-template <int SIZE, int COLS>
+template <int SIZE, int COLS, bool EARLY>
 struct LinearEpilogue {
+    static constexpr int kHeld = EARLY ? COLS : 32;   // columns held in registers
     static constexpr int kChunks = 32 * SIZE / 16;    // 16-byte chunks per step
     static constexpr int kUnit = 16 / SIZE;           // columns per chunk
 
@@ -413,16 +423,24 @@ struct LinearEpilogue {
         }
     }
 
-    // x0, row: the first column and this lane's row; taddr: the warp's accumulator
+    // x0, row: the first column and this lane's row; taddr: the warp's accumulator,
+    // and the barrier that releases it
     static __device__ __forceinline__ void run(const GemmArgs &g, int64_t x0, int64_t row,
-                                               uint32_t taddr, uint4 (&r)[kChunks])
+                                               uint32_t taddr, uint32_t release, uint4 (&r)[kChunks])
     {
         const bool f16 = g.epi.fmt == KQ_F16;
         uint8_t *const out = static_cast<uint8_t *>(g.epi.out) + row * g.epi.ldo * SIZE;
         // rows start on 32 bytes
         const bool wide = ((reinterpret_cast<uintptr_t>(g.epi.out) | static_cast<uintptr_t>(g.epi.ldo * SIZE)) & 31) == 0;
-        uint32_t a[32];
-        g_ld32_issue(taddr, a);
+        uint32_t a[kHeld];
+#pragma unroll
+        for (int c = 0; c < kHeld; c += 32) g_ld32_issue(taddr + c, a + c);
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int c = 0; c < kHeld; c += 32) g_wait_ld32(a + c);
+            g_fence_before();
+            mbar_arrive(release);
+        }
 #pragma unroll 1
         for (int c = 0; c < COLS / 32; ++c) {
             const int64_t col = x0 + 32 * c;
@@ -443,10 +461,15 @@ struct LinearEpilogue {
                 for (int j = 0; j < 32; ++j)
                     v[j] = g.epi.bias != nullptr && col + j < g.n ? __ldg(g.epi.bias + col + j) : 0.f;
             }
-            g_wait_ld32(a);
+            if constexpr (!EARLY) g_wait_ld32(a);
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(a[j]);
-            if (c + 1 < COLS / 32) g_ld32_issue(taddr + 32 * (c + 1), a);
+            if constexpr (EARLY) {
+#pragma unroll
+                for (int j = 0; j + 32 < kHeld; ++j) a[j] = a[j + 32];
+            } else if (c + 1 < COLS / 32) {
+                g_ld32_issue(taddr + 32 * (c + 1), a);
+            }
             apply_act(v, g.epi.act);
             if (row < g.m) {
                 if (g.epi.residual != nullptr) {
@@ -493,7 +516,11 @@ struct LinearEpilogue {
                 }
             }
         }
-        g_wait_ld32(a);                                    // a step that was not used
+        if constexpr (!EARLY) {
+            g_wait_ld32(a);                                // a step that was not used
+            g_fence_before();
+            mbar_arrive(release);
+        }
     }
 };
 
@@ -514,6 +541,8 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
     const uint32_t acc_full = bar + 16 * kXStages, acc_empty = acc_full + 16;
     const uint32_t tmem_slot = acc_empty + 16;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // role 0 producer, 1 MMA, 2... epilogue, -1 none
+    const int role = EPI == 0 ? warp : (warp < 8 ? warp + 2 : (warp < 10 ? warp - 8 : -1));
     const int64_t tiles = g.mtiles * g.ntiles;
     const int64_t wrt = (g.n + 127) / 128;            // 128-row scale tiles of W
 
@@ -531,7 +560,7 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
         }
         mbar_fence_init();
     }
-    if (warp == 1) g_tmem_alloc(tmem_slot, kXTmemCols);
+    if (role == 1) g_tmem_alloc(tmem_slot, kXTmemCols);
     g_fence_before();
     __syncthreads();
     g_fence_after();
@@ -539,7 +568,8 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem_base) : "r"(tmem_slot) : "memory");
     grid_dependency_wait();
 
-    if (warp == 0) {
+    if (role == 0) {
+        if constexpr (EPI != 0) regs_dec<kEpiRegsOther>();
         if (lane == 0) {
             int64_t kk = 0;
             bool ok = true;
@@ -583,7 +613,10 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
                 (void)mbar_wait(full + 8 * static_cast<int>(j % kXStages),
                                 static_cast<uint32_t>((j / kXStages) & 1));
         }
-    } else if (warp == 1) {
+    } else if (role < 0) {
+        if constexpr (EPI != 0) regs_dec<kEpiRegsOther>();
+    } else if (role == 1) {
+        if constexpr (EPI != 0) regs_dec<kEpiRegsOther>();
         // MMA issuer: the whole warp runs the loop, so that descriptors and
         // addresses are warp-uniform values; one elected lane issues a
         // stage's scale copies (A tile, then W's halves, per scale tile at)
@@ -711,16 +744,18 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
     } else {
         // epilogue: warp w reads TMEM lanes 32 (w % 4) .. + 31 and the 128
         // columns of half h = (w - 2) / 4 of the tile
-        const int qtr = warp & 3, h = (warp - 2) >> 2;
+        if constexpr (EPI != 0) regs_inc<kEpiRegs>();
+        const int qtr = warp & 3, h = (role - 2) >> 2;
         const uint32_t stg = base + C::kStagingOff +
-                             static_cast<uint32_t>(C::kBoxBufs * C::kBoxBytes * (warp - 2));
+                             static_cast<uint32_t>(C::kBoxBufs * C::kBoxBytes * (role - 2));
         int64_t tc = 0, nbox = 0;
         for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
             const int b = static_cast<int>(tc % C::kAccBufs);
             const int64_t erow = t / g.ntiles * 128 + 32 * qtr + lane;
             const int64_t ecol = t % g.ntiles * kXBN + C::kEpiCols * h;
             uint4 resid[EPI != 0 ? 2 * EPI : 1];
-            if constexpr (EPI != 0) LinearEpilogue<EPI, C::kEpiCols>::fetch(g, erow, ecol, resid);
+            using Epilogue = LinearEpilogue<EPI != 0 ? EPI : 2, C::kEpiCols, C::kAccBufs == 1>;
+            if constexpr (EPI != 0) Epilogue::fetch(g, erow, ecol, resid);
             const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full + 8 * b,
                                                               static_cast<uint32_t>((tc / C::kAccBufs) & 1)));
             if (!ok) break;
@@ -728,9 +763,7 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
             if constexpr (EPI != 0) {
                 const uint32_t acc = tmem_base + (static_cast<uint32_t>(qtr * 32) << 16) +
                                      static_cast<uint32_t>(kXBN * b + C::kEpiCols * h);
-                LinearEpilogue<EPI, C::kEpiCols>::run(g, ecol, erow, acc, resid);
-                g_fence_before();
-                mbar_arrive(acc_empty + 8 * b);
+                Epilogue::run(g, ecol, erow, acc, acc_empty + 8 * b, resid);
                 continue;
             }
             uint32_t v[128];
@@ -833,7 +866,7 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
 
     g_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (role == 1) {
         g_fence_after();
         g_tmem_dealloc(tmem_base, kXTmemCols);
     }
@@ -1080,14 +1113,13 @@ kq_status launch_linear_tiles(const LinearCall &q, cudaStream_t stream)
     kq_status st = device_info(info);
     if (st != KQ_OK) return st;
     const int64_t bk = mx ? 256 : 64, mtiles = (m + 127) / 128, ksteps = (k + bk - 1) / bk;
-    // the products' wave model; with a single accumulator (mx) the wide tile's
-    // epilogue is exposed whole
+    // the products' wave model; the 16-bit wide tile has two accumulators
     auto cost = [&](int64_t bn, double per_stage, double per_tile) {
         const int64_t tiles = mtiles * ((n + bn - 1) / bn);
         const int64_t waves = (tiles + info.sm_count - 1) / info.sm_count;
         return static_cast<double>(waves) * (static_cast<double>(ksteps) * per_stage + per_tile);
     };
-    const bool wide = cost(256, 1.35, mx ? 6.0 : 1.0) < cost(128, 1.0, 0.5);
+    const bool wide = cost(256, 1.35, mx ? 2.0 : 1.0) < cost(128, 1.0, 0.5);
     const int bn = wide ? 256 : 128;
     CUtensorMap ma, mw, mc;
     if (mx) {

@@ -98,6 +98,19 @@ __device__ __forceinline__ void g_wait_ld32(uint32_t *r)
                  : "memory");
 }
 
+// Registers per thread of the calling warpgroup (every one of its warps calls it).
+// What one group takes, others have to give: the sum stays what the launch gave.
+template <int N>
+__device__ __forceinline__ void regs_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 32 bytes to a 32-byte aligned address.
 __device__ __forceinline__ void stg256(void *p, const uint32_t *r)
 {
