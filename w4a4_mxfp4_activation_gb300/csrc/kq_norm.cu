@@ -212,7 +212,7 @@ struct NormArgs {
     int vec;                     // every parameter row is 16-byte aligned
     float eps, inv_d;
     float *mean, *rstd;          // written (forward, may be null) or read (backward)
-    int64_t run;                 // forward: consecutive rows of a team
+    int run;                     // forward: consecutive rows of a team
     int parts;                   // backward: row slices per group
     int stages;                  // rows in a team's ring
     float *dweight, *dbias;      // backward, [groups][d], may be null
@@ -226,29 +226,32 @@ struct Team {
     static constexpr int kRed = TPR > 32 ? kPerBlock * 2 * (TPR / 32) : 1;
 };
 
-// A ring of rows in shared memory, filled by bulk copies that thread 0 of the
-// team issues.  A ragged last chunk is copied whole: what follows it in its
-// row's pitch belongs to the buffer, and is masked.  In the matrix's last row,
-// where nothing need follow, thread 0 stores the chunk's elements itself.
-template <int FMT>
+// A ring of rows in shared memory (a power of two of them), filled by bulk copies
+// that thread 0 of the team issues.  A ragged last chunk is copied whole: what
+// follows it in its row's pitch belongs to the buffer, and is masked.  In the
+// matrix's last row, where nothing need follow, thread 0 stores the chunk's elements
+// itself.
+template <int FMT, bool RAG>
 struct Ring {
     uint32_t base, bar, row_bytes;
-    int stages;
 
     __device__ __forceinline__ void put(const uint8_t *src, uint32_t dst, uint32_t whole, int tail,
                                         uint32_t mbar) const
     {
         if (whole) bulk_load(dst, src, whole, mbar);
-        for (int i = 0; i < tail; ++i) {
-            constexpr int SIZE = Chunk<FMT>::kSize;
-            if constexpr (SIZE == 4)
-                asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + whole + 4 * i),
-                             "r"(reinterpret_cast<const uint32_t *>(src + whole)[i])
-                             : "memory");
-            else
-                asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + whole + 2 * i),
-                             "h"(reinterpret_cast<const uint16_t *>(src + whole)[i])
-                             : "memory");
+        if constexpr (RAG) {
+#pragma unroll 1
+            for (int i = 0; i < tail; ++i) {
+                constexpr int SIZE = Chunk<FMT>::kSize;
+                if constexpr (SIZE == 4)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst + whole + 4 * i),
+                                 "r"(reinterpret_cast<const uint32_t *>(src + whole)[i])
+                                 : "memory");
+                else
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(dst + whole + 2 * i),
+                                 "h"(reinterpret_cast<const uint16_t *>(src + whole)[i])
+                                 : "memory");
+            }
         }
     }
     // Fills stage s with a row of x, and one of y after it unless y is null.
@@ -256,8 +259,9 @@ struct Ring {
                                          int d) const
     {
         constexpr int N = Chunk<FMT>::kN;
-        const uint32_t whole = last_row ? static_cast<uint32_t>(d / N) * 16u : row_bytes;
-        const int tail = last_row ? d % N : 0;
+        const bool cut = RAG && last_row;
+        const uint32_t whole = cut ? static_cast<uint32_t>(d / N) * 16u : row_bytes;
+        const int tail = cut ? d % N : 0;
         const uint32_t mbar = bar + 8 * s, rows = y ? 2u : 1u;
         const uint32_t dst = base + static_cast<uint32_t>(s) * rows * row_bytes;
         // the count is raised before the copies can complete; the one arrival
@@ -269,18 +273,12 @@ struct Ring {
         if (y) put(y, dst + row_bytes, whole, tail, mbar);
         mbar_arrive(mbar);
     }
-    __device__ __forceinline__ void init() const
+    // Waits for the last of `issued` rows into each stage (a wait gave up, and the
+    // block must not leave while copies are in flight).
+    __device__ __noinline__ void drain(int issued, int stages) const
     {
-        for (int s = 0; s < stages; ++s) mbar_init(bar + 8 * s, 1);
-        mbar_fence_init();
-    }
-    // Waits for every row from the first one up to `issued` (a wait gave up,
-    // and the block must not leave while copies are in flight).
-    __device__ __noinline__ void drain(int64_t issued) const
-    {
-        for (int64_t i = max(int64_t(0), issued - stages); i < issued; ++i)
-            (void)mbar_wait(bar + 8 * static_cast<int>(i % stages),
-                            static_cast<uint32_t>((i / stages) & 1));
+        for (int i = max(0, issued - stages); i < issued; ++i)
+            (void)mbar_wait(bar + 8 * (i & (stages - 1)), (i & stages) ? 1u : 0u);
     }
 };
 
@@ -291,8 +289,12 @@ constexpr uint32_t kNan = 0x7FC00000u;
 
 // A team takes a run of consecutive rows, two at a time: both rows' sums share
 // one reduction, and the parameters (8 bytes a channel, against 2 or 4 of x)
-// are fetched from the caches once for both.  Both rows are in registers before
-// the first reduction; after it their stages are filled again.
+// are fetched from the caches once for both.  Both rows are in registers, as fp32,
+// before the first reduction; after it their stages are filled again.  Teams are
+// small and threads take up to five chunks a row: what a row costs whatever its
+// length (reductions, barriers, the next copies) is then spread over 80 elements a
+// thread (three chunks by 64 threads: 20 instructions an element, 79 us on 65536 x
+// 1152 rows).
 template <int FMT, int TPR, int VPT, bool RAG>
 __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads)
     norm_forward_kernel(const NormArgs g)
@@ -303,69 +305,65 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
     extern __shared__ __align__(16) uint8_t ring_bytes[];   // [PB][stages][nc * 16]
     const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
     const int64_t first = (blockIdx.x * static_cast<int64_t>(PB) + team) * g.run;
-    const int64_t rows = min(g.run, g.m - first);           // may be <= 0
+    const int rows = static_cast<int>(min(static_cast<int64_t>(g.run), g.m - first));  // may be <= 0
     const int nc = (g.d + N - 1) / N, S = g.stages;
-    Ring<FMT> ring;
+    Ring<FMT, RAG> ring;
     ring.row_bytes = static_cast<uint32_t>(nc) * 16u;
-    ring.stages = S;
     ring.base = smem_addr(ring_bytes) + static_cast<uint32_t>(team * S) * ring.row_bytes;
     ring.bar = smem_addr(&bars[team][0]);
-    if (t == 0) ring.init();
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(ring.bar + 8 * s, 1);
+        mbar_fence_init();
+    }
     __syncthreads();
     grid_dependency_wait();
     if (rows <= 0) return;
 
-    // thread 0: the next row to copy, and its stage
-    int64_t issued = 0;
-    int fs = 0;
-    const uint8_t *xr = g.x + first * g.xpitch;
-    auto fill = [&] {
-        ring.fill(fs, xr, nullptr, first + issued + 1 == g.m, g.d);
-        xr += g.xpitch;
-        ++issued;
-        fs = fs + 1 == S ? 0 : fs + 1;
+    auto fill = [&](int i) {
+        if (i < rows)
+            ring.fill(i & (S - 1), g.x + (first + i) * g.xpitch, nullptr, first + i + 1 == g.m, g.d);
     };
     if (t == 0)
-        while (issued < S && issued < rows) fill();
+        for (int i = 0; i < S; ++i) fill(i);
     bool dead = false;                                      // a copy did not arrive in time
-    int s = 0;
-    uint32_t parity = 0;
-    uint8_t *yr = g.y + first * g.ypitch;
     // the group of the current row, and how many of its rows are left
     int64_t grp = first / g.group_rows, left = (grp + 1) * g.group_rows - first;
-    for (int64_t i = 0; i < rows; i += 2, yr += 2 * g.ypitch, left -= 2) {
+#pragma unroll 1
+    for (int i = 0; i < rows; i += 2, left -= 2) {
         while (left <= 0) {
             ++grp;
             left += g.group_rows;
         }
         const bool two = i + 1 < rows;
-        uint4 raw[2][VPT];
+        const int s = i & (S - 1);
+        const uint32_t parity = (i & S) ? 1u : 0u;
+        float2 v[2][VPT][P];
         if (!dead) dead = !mbar_wait(ring.bar + 8 * s, parity);
         if (!dead && two) dead = !mbar_wait(ring.bar + 8 * (s + 1), parity);
+        // an odd run's missing second row repeats the first
+        const uint32_t a0 = ring.base + static_cast<uint32_t>(s) * ring.row_bytes + 16 * t;
+        const uint32_t a1 = two ? a0 + ring.row_bytes : a0;
         float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = t + k * TPR;
+            if (c < nc) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                raw[r][k] = make_uint4(0, 0, 0, 0);
-                if (c < nc) {
-                    // an odd run's missing second row repeats the first
-                    const int st = r && two ? s + 1 : s;
-                    raw[r][k] = lds128(ring.base + static_cast<uint32_t>(st) * ring.row_bytes + 16 * c);
-                    float2 v[P];
-                    unpack<FMT>(raw[r][k], v);
-                    mask_tail<RAG>(v, c, g.d);
+                for (int r = 0; r < 2; ++r) {
+                    unpack<FMT>(lds128((r ? a1 : a0) + 16 * TPR * k), v[r][k]);
+                    mask_tail<RAG>(v[r][k], c, g.d);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) sum[r] = __fadd2_rn(sum[r], v[j]);
+                    for (int j = 0; j < P; ++j) sum[r] = __fadd2_rn(sum[r], v[r][k][j]);
                 }
             }
         }
         const float2 total =
             team_sum<TPR>(make_float2(sum[0].x + sum[0].y, sum[1].x + sum[1].y), red, team, 0);
         if (TPR == 32) __syncwarp();
-        if (t == 0 && !dead)
-            for (int r = 0; r < 2 && issued < rows; ++r) fill();
+        if (t == 0 && !dead) {
+            fill(i + S);
+            fill(i + S + 1);
+        }
         const float mean[2] = {total.x * g.inv_d, total.y * g.inv_d};
         float2 q[2] = {both(0.f), both(0.f)};
 #pragma unroll
@@ -374,13 +372,11 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
             if (c < nc) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    float2 v[P];
-                    unpack<FMT>(raw[r][k], v);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) v[j] = __fadd2_rn(v[j], both(-mean[r]));
-                    mask_tail<RAG>(v, c, g.d);
+                    for (int j = 0; j < P; ++j) v[r][k][j] = __fadd2_rn(v[r][k][j], both(-mean[r]));
+                    mask_tail<RAG>(v[r][k], c, g.d);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) q[r] = __ffma2_rn(v[j], v[j], q[r]);
+                    for (int j = 0; j < P; ++j) q[r] = __ffma2_rn(v[r][k][j], v[r][k][j], q[r]);
                 }
             }
         }
@@ -389,10 +385,10 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
         // rsqrtf is within 2 ulp, and its few instructions run in every thread
         float rstd[2] = {rsqrtf(var.x * g.inv_d + g.eps), rsqrtf(var.y * g.inv_d + g.eps)};
         if (dead) rstd[0] = rstd[1] = __uint_as_float(kNan);
-        const int64_t row = first + i;
         const bool same = left > 1;
         const float *w = g.weight ? g.weight + grp * g.d : nullptr;
         const float *b = g.bias ? g.bias + grp * g.d : nullptr;
+        uint8_t *yr = g.y + (first + i) * g.ypitch;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = t + k * TPR;
@@ -407,28 +403,19 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
                         load_param<P>(w ? w + g.d : nullptr, c, g.d, g.vec, 1.f, wv);
                         load_param<P>(b ? b + g.d : nullptr, c, g.d, g.vec, 0.f, bv);
                     }
-                    float2 v[P];
-                    unpack<FMT>(raw[r][k], v);
 #pragma unroll
-                    for (int j = 0; j < P; ++j) {
-                        const float2 z = __fmul2_rn(__fadd2_rn(v[j], both(-mean[r])), both(rstd[r]));
-                        v[j] = __ffma2_rn(z, wv[j], bv[j]);
-                    }
-                    store_chunk<FMT, RAG>(yr + r * g.ypitch, c, g.d, pack<FMT>(v));
+                    for (int j = 0; j < P; ++j)
+                        v[r][k][j] = __ffma2_rn(__fmul2_rn(v[r][k][j], both(rstd[r])), wv[j], bv[j]);
+                    store_chunk<FMT, RAG>(yr + r * g.ypitch, c, g.d, pack<FMT>(v[r][k]));
                 }
             }
         }
         if (t < 2 && i + t < rows) {
-            if (g.mean) g.mean[row + t] = mean[t];
-            if (g.rstd) g.rstd[row + t] = rstd[t];
-        }
-        s += 2;
-        if (s >= S) {
-            s = 0;
-            parity ^= 1;
+            if (g.mean) g.mean[first + i + t] = t ? mean[1] : mean[0];
+            if (g.rstd) g.rstd[first + i + t] = t ? rstd[1] : rstd[0];
         }
     }
-    if (t == 0 && dead) ring.drain(issued);
+    if (t == 0 && dead) ring.drain(rows, S);
 }
 
 // ---- backward -------------------------------------------------------------------
@@ -451,31 +438,28 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
     const int p = static_cast<int>(blockIdx.x % static_cast<unsigned>(g.parts));
     const int64_t last = min(g.m, (gi + 1) * g.group_rows);
     const int64_t first = gi * g.group_rows + static_cast<int64_t>(p) * PB + team;
-    const int64_t step = static_cast<int64_t>(g.parts) * PB;
-    const int64_t rows = first < last ? (last - first + step - 1) / step : 0;
+    const int step = g.parts * PB;
+    const int rows = first < last ? static_cast<int>((last - first + step - 1) / step) : 0;
     const int nc = (g.d + N - 1) / N, S = g.stages;
-    Ring<FMT> ring;
+    Ring<FMT, RAG> ring;
     ring.row_bytes = static_cast<uint32_t>(nc) * 16u;
-    ring.stages = S;
     ring.base = smem_addr(ring_bytes) + static_cast<uint32_t>(team * S) * 2u * ring.row_bytes;
     ring.bar = smem_addr(&bars[team][0]);
-    if (t == 0) ring.init();
+    if (t == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(ring.bar + 8 * s, 1);
+        mbar_fence_init();
+    }
     __syncthreads();
     grid_dependency_wait();
 
-    // thread 0: the next row to copy, and its stage
-    int64_t issued = 0;
-    int fs = 0;
-    const uint8_t *xr = g.x + first * g.xpitch, *dyr = g.dy + first * g.dypitch;
-    auto fill = [&] {
-        ring.fill(fs, xr, dyr, first + issued * step + 1 == g.m, g.d);
-        xr += step * g.xpitch;
-        dyr += step * g.dypitch;
-        ++issued;
-        fs = fs + 1 == S ? 0 : fs + 1;
+    auto fill = [&](int i) {
+        if (i < rows) {
+            const int64_t row = first + static_cast<int64_t>(i) * step;
+            ring.fill(i & (S - 1), g.x + row * g.xpitch, g.dy + row * g.dypitch, row + 1 == g.m, g.d);
+        }
     };
     if (t == 0)
-        while (issued < S && issued < rows) fill();
+        for (int i = 0; i < S; ++i) fill(i);
 
     float2 wv[VPT][P], aw[VPT][P], ab[VPT][P];
 #pragma unroll
@@ -486,20 +470,20 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
         if (c < nc) load_param<P>(g.weight ? g.weight + gi * g.d : nullptr, c, g.d, g.vec, 1.f, wv[k]);
     }
     float mean32 = 0.f, rstd32 = 0.f;           // of row 32 (i / 32) + lane of this team
-    int s = 0, buf = 0;
-    uint32_t parity = 0;
     bool dead = false;                          // a copy did not arrive in time
-    uint8_t *yr = g.y + first * g.ypitch;
-    for (int64_t i = 0; i < rows; ++i, yr += step * g.ypitch) {
+#pragma unroll 1
+    for (int i = 0; i < rows; ++i) {
         if ((i & 31) == 0 && i + lane < rows) {
-            mean32 = __ldg(g.mean + first + (i + lane) * step);
-            rstd32 = __ldg(g.rstd + first + (i + lane) * step);
+            const int64_t row = first + static_cast<int64_t>(i + lane) * step;
+            mean32 = __ldg(g.mean + row);
+            rstd32 = __ldg(g.rstd + row);
         }
-        float mean = __shfl_sync(0xffffffffu, mean32, static_cast<int>(i & 31));
-        const float rstd = __shfl_sync(0xffffffffu, rstd32, static_cast<int>(i & 31));
-        if (!dead) dead = !mbar_wait(ring.bar + 8 * s, parity);
+        float mean = __shfl_sync(0xffffffffu, mean32, i & 31);
+        const float rstd = __shfl_sync(0xffffffffu, rstd32, i & 31);
+        const int s = i & (S - 1);
+        if (!dead) dead = !mbar_wait(ring.bar + 8 * s, (i & S) ? 1u : 0u);
         if (dead) mean = __uint_as_float(kNan);
-        const uint32_t sx = ring.base + static_cast<uint32_t>(s) * 2u * ring.row_bytes;
+        const uint32_t sx = ring.base + static_cast<uint32_t>(s) * 2u * ring.row_bytes + 16 * t;
         const uint32_t sd = sx + ring.row_bytes;
         uint4 rx[VPT], rd[VPT];
         // dy and z of chunk k; zeros past column d
@@ -516,10 +500,9 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const int c = t + k * TPR;
-            rx[k] = rd[k] = make_uint4(0, 0, 0, 0);
             if (c < nc) {
-                rx[k] = lds128(sx + 16 * c);
-                rd[k] = lds128(sd + 16 * c);
+                rx[k] = lds128(sx + 16 * TPR * k);
+                rd[k] = lds128(sd + 16 * TPR * k);
                 float2 dy[P], z[P];
                 chunk(k, dy, z);
 #pragma unroll
@@ -532,13 +515,13 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
                 }
             }
         }
-        const float2 sum = team_sum<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red, team, buf);
+        const float2 sum = team_sum<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red, team, i & 1);
         if (TPR == 32) __syncwarp();
-        // this row's stage: the row is in registers
-        if (t == 0 && issued < rows && !dead) fill();
+        if (t == 0 && !dead) fill(i + S);       // this row's stage: the row is in registers
         if (g.y) {
             // rstd * (g - sum(g) / d - z * sum(g z) / d)
             const float2 c1 = both(-sum.x * g.inv_d), c2 = both(-sum.y * g.inv_d);
+            uint8_t *yr = g.y + (first + static_cast<int64_t>(i) * step) * g.ypitch;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const int c = t + k * TPR;
@@ -552,13 +535,8 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
                 }
             }
         }
-        buf ^= 1;
-        if (++s == S) {
-            s = 0;
-            parity ^= 1;
-        }
     }
-    if (t == 0 && dead) ring.drain(issued);
+    if (t == 0 && dead) ring.drain(rows, S);
     if (g.dweight == nullptr && g.dbias == nullptr) return;
     __syncthreads();
     float *sums = reinterpret_cast<float *>(ring_bytes);      // [2][d], PB > 1 only
@@ -628,8 +606,8 @@ __global__ void __launch_bounds__(512) norm_reduce_kernel(const NormArgs g)
 
 constexpr int kSmemMost = 224 * 1024;
 
-// A kernel's setup and the stages of its ring: as many as fit the share of
-// shared memory of a block where an SM holds 512 threads, 4 at most.
+// A kernel's setup and the stages of its ring: 4, 2 or 1, as many as fit the share
+// of shared memory of a block where an SM holds 512 threads.
 template <int FMT, int TPR, typename Kernel>
 kq_status ring_setup(Kernel kern, DeviceOnce &once, NormArgs &g, int rows_per_stage, int &stage)
 {
@@ -639,7 +617,8 @@ kq_status ring_setup(Kernel kern, DeviceOnce &once, NormArgs &g, int rows_per_st
     constexpr int kResident = std::max(1, 512 / Team<TPR>::kThreads);
     const int nc = (g.d + Chunk<FMT>::kN - 1) / Chunk<FMT>::kN;
     stage = Team<TPR>::kPerBlock * rows_per_stage * 16 * nc;
-    g.stages = std::min(kMaxStages, kSmemMost / kResident / stage);
+    const int fit = kSmemMost / kResident / stage;
+    g.stages = fit >= kMaxStages ? kMaxStages : fit >= 2 ? 2 : 1;
     return st;
 }
 
@@ -652,26 +631,28 @@ kq_status forward_t(NormArgs &g, cudaStream_t stream)
     int stage;
     const kq_status st = ring_setup<FMT, TPR>(kern, once, g, 1, stage);
     if (st != KQ_OK) return st;
-    g.stages &= ~1;                                  // rows go two at a time
-    // one wave of teams, an even number of rows each
+    // one wave of teams, an even number of rows each (rows go two at a time; the
+    // longest row leaves room for two)
     const int64_t teams = static_cast<int64_t>(152) * kResident * PB;
-    g.run = std::max<int64_t>(1, (g.m + teams - 1) / teams);
-    if (g.run > 1) g.run += g.run & 1;
-    const int64_t blocks = (g.m + g.run * PB - 1) / (g.run * PB);
+    int64_t run = std::max<int64_t>(1, (g.m + teams - 1) / teams);
+    if (run > 1) run += run & 1;
+    g.run = static_cast<int>(run);
+    const int64_t blocks = (g.m + run * PB - 1) / (run * PB);
     return launch_pdl(kern, static_cast<int>(blocks), Team<TPR>::kThreads,
                       static_cast<size_t>(g.stages * stage), stream, g);
 }
 
-// A team is the smallest that holds a row in three chunks a thread.
+// A team is the smallest that holds a row in five chunks a thread (the longest rows
+// of 32-bit elements: four, by 1024 threads).
 template <int FMT, bool RAG>
 kq_status forward_f(NormArgs &g, cudaStream_t stream)
 {
     const int nc = (g.d + Chunk<FMT>::kN - 1) / Chunk<FMT>::kN;
     if (nc <= 96) return forward_t<FMT, 32, 3, RAG>(g, stream);
-    if (nc <= 192) return forward_t<FMT, 64, 3, RAG>(g, stream);
-    if (nc <= 384) return forward_t<FMT, 128, 3, RAG>(g, stream);
-    if (nc <= 768) return forward_t<FMT, 256, 3, RAG>(g, stream);
-    if (nc <= 1536) return forward_t<FMT, 512, 3, RAG>(g, stream);
+    if (nc <= 160) return forward_t<FMT, 32, 5, RAG>(g, stream);
+    if (nc <= 320) return forward_t<FMT, 64, 5, RAG>(g, stream);
+    if (nc <= 640) return forward_t<FMT, 128, 5, RAG>(g, stream);
+    if (nc <= 1280) return forward_t<FMT, 256, 5, RAG>(g, stream);
     if (nc <= 2048) return forward_t<FMT, 512, 4, RAG>(g, stream);
     if constexpr (FMT == KQ_F32) return forward_t<FMT, 1024, 4, RAG>(g, stream);
     return KQ_ERR_SHAPE;
