@@ -124,7 +124,7 @@ size_t kq_layer_norm_backward_bytes(int64_t m, int64_t d, int64_t group_rows)
     const int64_t parts = norm_parts(m, group_rows == 0 ? m : group_rows);
     if (parts <= 1) return 0;
     return static_cast<size_t>(norm_groups(m, group_rows)) * static_cast<size_t>(parts) * 2u *
-           static_cast<size_t>(d) * sizeof(float);
+           static_cast<size_t>((d + 7) / 8 * 8) * sizeof(float);
 }
 
 kq_status kq_w4a4_linear(const uint8_t *qa, int64_t ldqa, const uint8_t *sfa, const uint8_t *qw,

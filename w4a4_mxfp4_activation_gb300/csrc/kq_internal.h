@@ -134,7 +134,7 @@ kq_status launch_layer_error(const float *c, int64_t ldc, const float *r, int64_
                              int64_t n, double *out, cudaStream_t stream);
 
 // Layer norm; group_rows > 0.  norm_parts: row slices per group of the
-// backward pass (its workspace is [groups][parts][2][d] fp32 when parts > 1).
+// backward pass (its workspace is [groups][parts][2][d rounded up] fp32 when parts > 1).
 int64_t norm_parts(int64_t m, int64_t group_rows);
 kq_status launch_norm_forward(const void *x, int64_t ldx, kq_format fmt, int64_t m, int64_t d,
                               const float *weight, const float *bias, int64_t group_rows, float eps,

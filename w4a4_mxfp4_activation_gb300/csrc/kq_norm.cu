@@ -146,13 +146,14 @@ __device__ __forceinline__ void load_param(const float *p, int c, int d, bool ve
     }
 }
 
-// Barrier of a team of TPR threads; its id is an immediate, because a block
-// that computes ids is charged all 16 barriers and four such fill an SM.
-template <int TPR>
+// Barrier of a team of TPR threads.  In blocks of two teams the id is an immediate:
+// a block that computes ids is charged all 16 barriers, and four such fill an SM.
+template <int TPR, int PB>
 __device__ __forceinline__ void team_barrier(int team)
 {
-    static_assert(TPR >= 64, "at most two teams a block");
-    if (TPR >= 128 || team == 0)
+    if constexpr (PB > 2)
+        named_barrier(1 + static_cast<uint32_t>(team), TPR);
+    else if (PB == 1 || team == 0)
         asm volatile("bar.sync 1, %0;" ::"n"(TPR) : "memory");
     else
         asm volatile("bar.sync 2, %0;" ::"n"(TPR) : "memory");
@@ -162,7 +163,7 @@ __device__ __forceinline__ void team_barrier(int team)
 // half warp with one of the two sums, so that a warp takes five shuffles and
 // not ten; `red` holds the warps' sums of one row, and `buf` alternates from
 // sum to sum so that one barrier per sum is enough.
-template <int TPR>
+template <int TPR, int PB>
 __device__ __forceinline__ float2 team_sum(float2 v, float2 *red, int team, int buf)
 {
     const int lane = threadIdx.x & 31;
@@ -179,7 +180,7 @@ __device__ __forceinline__ float2 team_sum(float2 v, float2 *red, int team, int 
         float2 *r = red + (team * 2 + buf) * W;
         const int warp = (threadIdx.x % TPR) >> 5;
         if ((lane & 15) == 0) reinterpret_cast<float *>(r + warp)[lane >> 4] = a;
-        team_barrier<TPR>(team);
+        team_barrier<TPR, PB>(team);
         if constexpr (W <= 8) {
             v = r[0];
 #pragma unroll
@@ -216,15 +217,22 @@ struct NormArgs {
     int parts;                   // backward: row slices per group
     int stages;                  // rows in a team's ring
     float *dweight, *dbias;      // backward, [groups][d], may be null
-    float *work;                 // backward: [groups][parts][2][d] when parts > 1
+    float *work;                 // backward: [groups][parts][2][pitch] when parts > 1
 };
 
-template <int TPR>
+// Teams of TPR threads in blocks of BLOCK threads, or one in a block of its own size.
+template <int TPR, int BLOCK>
 struct Team {
-    static constexpr int kPerBlock = TPR >= 128 ? 1 : 128 / TPR;
+    static constexpr int kPerBlock = TPR >= BLOCK ? 1 : BLOCK / TPR;
     static constexpr int kThreads = TPR * kPerBlock;
     static constexpr int kRed = TPR > 32 ? kPerBlock * 2 * (TPR / 32) : 1;
 };
+// Forward: small blocks, as many as an SM holds.  Backward: one block an SM, so that
+// the column sums leave it once.
+template <int TPR>
+using FwdTeam = Team<TPR, 128>;
+template <int TPR>
+using BwdTeam = Team<TPR, 512>;
 
 // A ring of rows in shared memory (a power of two of them), filled by bulk copies
 // that thread 0 of the team issues.  A ragged last chunk is copied whole: what
@@ -296,11 +304,11 @@ constexpr uint32_t kNan = 0x7FC00000u;
 // thread (three chunks by 64 threads: 20 instructions an element, 79 us on 65536 x
 // 1152 rows).
 template <int FMT, int TPR, int VPT, bool RAG>
-__global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads)
+__global__ void __launch_bounds__(FwdTeam<TPR>::kThreads, 512 / FwdTeam<TPR>::kThreads)
     norm_forward_kernel(const NormArgs g)
 {
-    constexpr int N = Chunk<FMT>::kN, P = N / 2, PB = Team<TPR>::kPerBlock;
-    __shared__ float2 red[Team<TPR>::kRed];
+    constexpr int N = Chunk<FMT>::kN, P = N / 2, PB = FwdTeam<TPR>::kPerBlock;
+    __shared__ float2 red[FwdTeam<TPR>::kRed];
     __shared__ __align__(8) uint64_t bars[PB][kMaxStages];
     extern __shared__ __align__(16) uint8_t ring_bytes[];   // [PB][stages][nc * 16]
     const int team = threadIdx.x / TPR, t = threadIdx.x % TPR;
@@ -358,7 +366,7 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
             }
         }
         const float2 total =
-            team_sum<TPR>(make_float2(sum[0].x + sum[0].y, sum[1].x + sum[1].y), red, team, 0);
+            team_sum<TPR, PB>(make_float2(sum[0].x + sum[0].y, sum[1].x + sum[1].y), red, team, 0);
         if (TPR == 32) __syncwarp();
         if (t == 0 && !dead) {
             fill(i + S);
@@ -381,7 +389,7 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
             }
         }
         const float2 var =
-            team_sum<TPR>(make_float2(q[0].x + q[0].y, q[1].x + q[1].y), red, team, 1);
+            team_sum<TPR, PB>(make_float2(q[0].x + q[0].y, q[1].x + q[1].y), red, team, 1);
         // rsqrtf is within 2 ulp, and its few instructions run in every thread
         float rstd[2] = {rsqrtf(var.x * g.inv_d + g.eps), rsqrtf(var.y * g.inv_d + g.eps)};
         if (dead) rstd[0] = rstd[1] = __uint_as_float(kNan);
@@ -420,17 +428,53 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
 
 // ---- backward -------------------------------------------------------------------
 
+// All ones where the last chunk of a row of d elements has an element.
+template <int FMT>
+__device__ __forceinline__ uint4 tail_mask(int d)
+{
+    constexpr int N = Chunk<FMT>::kN, SIZE = Chunk<FMT>::kSize;
+    const int bytes = (d % N ? d % N : N) * SIZE;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] = bytes >= 4 * i + 4 ? ~0u : bytes <= 4 * i ? 0u : (1u << (8 * (bytes - 4 * i))) - 1u;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 keep(const uint4 &v, bool cut, const uint4 &m)
+{
+    return make_uint4(cut ? v.x & m.x : v.x, cut ? v.y & m.y : v.y, cut ? v.z & m.z : v.z,
+                      cut ? v.w & m.w : v.w);
+}
+
+template <int P>
+__device__ __forceinline__ void put_floats(float *o, const float2 (&v)[P])
+{
+#pragma unroll
+    for (int j = 0; j < P; j += 2)
+        *reinterpret_cast<float4 *>(o + 2 * j) = make_float4(v[j].x, v[j].y, v[j + 1].x, v[j + 1].y);
+}
+template <int P>
+__device__ __forceinline__ void add_floats(const float *o, float2 (&v)[P])
+{
+#pragma unroll
+    for (int j = 0; j < P; j += 2) {
+        const float4 f = *reinterpret_cast<const float4 *>(o + 2 * j);
+        v[j] = __fadd2_rn(v[j], make_float2(f.x, f.y));
+        v[j + 1] = __fadd2_rn(v[j + 1], make_float2(f.z, f.w));
+    }
+}
+
 // A block takes slice p of group gi; its teams walk the rows of the slice.  The
 // group's weights and the columns' sums of dy * z and dy stay in registers; the
 // teams' sums are added in team order at the end, so the result does not depend
 // on timing.  The saved statistics of the next 32 rows are fetched by the lanes
 // of each warp at once: one load a row would put its latency into every row.
 template <int FMT, int TPR, int VPT, bool RAG>
-__global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads)
+__global__ void __launch_bounds__(BwdTeam<TPR>::kThreads, 1)
     norm_backward_kernel(const NormArgs g)
 {
-    constexpr int N = Chunk<FMT>::kN, P = N / 2, PB = Team<TPR>::kPerBlock;
-    __shared__ float2 red[Team<TPR>::kRed];
+    constexpr int N = Chunk<FMT>::kN, P = N / 2, PB = BwdTeam<TPR>::kPerBlock;
+    __shared__ float2 red[BwdTeam<TPR>::kRed];
     __shared__ __align__(8) uint64_t bars[PB][kMaxStages];
     extern __shared__ __align__(16) uint8_t ring_bytes[];   // [PB][stages][2][nc * 16]
     const int team = threadIdx.x / TPR, t = threadIdx.x % TPR, lane = threadIdx.x & 31;
@@ -469,6 +513,7 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
         for (int j = 0; j < P; ++j) wv[k][j] = aw[k][j] = ab[k][j] = both(0.f);
         if (c < nc) load_param<P>(g.weight ? g.weight + gi * g.d : nullptr, c, g.d, g.vec, 1.f, wv[k]);
     }
+    const uint4 tail = tail_mask<FMT>(g.d);
     float mean32 = 0.f, rstd32 = 0.f;           // of row 32 (i / 32) + lane of this team
     bool dead = false;                          // a copy did not arrive in time
 #pragma unroll 1
@@ -486,15 +531,14 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
         const uint32_t sx = ring.base + static_cast<uint32_t>(s) * 2u * ring.row_bytes + 16 * t;
         const uint32_t sd = sx + ring.row_bytes;
         uint4 rx[VPT], rd[VPT];
-        // dy and z of chunk k; zeros past column d
+        // dy and z of chunk k; past column d x and dy were cleared, so that g, g z and
+        // the column sums are zero there
         auto chunk = [&](int k, float2(&dy)[P], float2(&z)[P]) {
             unpack<FMT>(rx[k], z);
             unpack<FMT>(rd[k], dy);
 #pragma unroll
             for (int j = 0; j < P; ++j)
                 z[j] = __fmul2_rn(__fadd2_rn(z[j], both(-mean)), both(rstd));
-            mask_tail<RAG>(z, t + k * TPR, g.d);
-            mask_tail<RAG>(dy, t + k * TPR, g.d);
         };
         float2 s1 = both(0.f), s2 = both(0.f);
 #pragma unroll
@@ -503,6 +547,11 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
             if (c < nc) {
                 rx[k] = lds128(sx + 16 * TPR * k);
                 rd[k] = lds128(sd + 16 * TPR * k);
+                if constexpr (RAG) {
+                    const bool cut = c == nc - 1;
+                    rx[k] = keep(rx[k], cut, tail);
+                    rd[k] = keep(rd[k], cut, tail);
+                }
                 float2 dy[P], z[P];
                 chunk(k, dy, z);
 #pragma unroll
@@ -515,7 +564,7 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
                 }
             }
         }
-        const float2 sum = team_sum<TPR>(make_float2(s1.x + s1.y, s2.x + s2.y), red, team, i & 1);
+        const float2 sum = team_sum<TPR, PB>(make_float2(s1.x + s1.y, s2.x + s2.y), red, team, i & 1);
         if (TPR == 32) __syncwarp();
         if (t == 0 && !dead) fill(i + S);       // this row's stage: the row is in registers
         if (g.y) {
@@ -538,69 +587,92 @@ __global__ void __launch_bounds__(Team<TPR>::kThreads, 512 / Team<TPR>::kThreads
     }
     if (t == 0 && dead) ring.drain(rows, S);
     if (g.dweight == nullptr && g.dbias == nullptr) return;
-    __syncthreads();
-    float *sums = reinterpret_cast<float *>(ring_bytes);      // [2][d], PB > 1 only
-    float *ow, *ob;
-    if (g.parts > 1) {
-        ow = g.work + (gi * g.parts + p) * 2 * static_cast<int64_t>(g.d);
-        ob = ow + g.d;
-    } else {
-        ow = g.dweight ? g.dweight + gi * g.d : nullptr;
-        ob = g.dbias ? g.dbias + gi * g.d : nullptr;
-    }
-    for (int k = 0; k < PB; ++k) {
-        if (team == k) {
+    // the teams' sums, halving their number: the upper half's go through shared
+    // memory ([teams][2][pitch]); then the block's, in rows of whole chunks
+    const int pitch = nc * N;
+    float *const sums = reinterpret_cast<float *>(ring_bytes);
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
+    for (int half = PB / 2; half >= 1; half /= 2) {
+        __syncthreads();
+        if (team >= half && team < 2 * half) {
+            float *o = sums + (team - half) * 2 * pitch;
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int col = (t + i * TPR) * N + j;
-                    if (col < g.d) {
-                        float a = j & 1 ? aw[i][j / 2].y : aw[i][j / 2].x;
-                        float b = j & 1 ? ab[i][j / 2].y : ab[i][j / 2].x;
-                        if (k > 0) {
-                            a += sums[col];
-                            b += sums[g.d + col];
-                        }
-                        if (k < PB - 1) {
-                            sums[col] = a;
-                            sums[g.d + col] = b;
-                        } else {
-                            if (ow) ow[col] = a;
-                            if (ob) ob[col] = b;
-                        }
-                    }
+            for (int k = 0; k < VPT; ++k) {
+                const int c = t + k * TPR;
+                if (c < nc) {
+                    put_floats<P>(o + c * N, aw[k]);
+                    put_floats<P>(o + pitch + c * N, ab[k]);
                 }
             }
         }
-        if (k < PB - 1) __syncthreads();
+        __syncthreads();
+        if (team < half) {
+            const float *o = sums + team * 2 * pitch;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int c = t + k * TPR;
+                if (c < nc) {
+                    add_floats<P>(o + c * N, aw[k]);
+                    add_floats<P>(o + pitch + c * N, ab[k]);
+                }
+            }
+        }
+    }
+    if (team != 0) return;
+    if (g.parts > 1) {
+        float *o = g.work + (gi * g.parts + p) * 2 * static_cast<int64_t>(pitch);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int c = t + k * TPR;
+            if (c < nc) {
+                put_floats<P>(o + c * N, aw[k]);
+                put_floats<P>(o + pitch + c * N, ab[k]);
+            }
+        }
+        return;
+    }
+    float *ow = g.dweight ? g.dweight + gi * g.d : nullptr;
+    float *ob = g.dbias ? g.dbias + gi * g.d : nullptr;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int col = (t + k * TPR) * N + j;
+            if (col < g.d) {
+                if (ow) ow[col] = j & 1 ? aw[k][j / 2].y : aw[k][j / 2].x;
+                if (ob) ob[col] = j & 1 ? ab[k][j / 2].y : ab[k][j / 2].x;
+            }
+        }
     }
 }
 
-// dw and db from the slices' sums.  A block takes 32 neighbouring columns; its
-// 16 warps take every 16th slice each, and the warps' sums are added in order.
-__global__ void __launch_bounds__(512) norm_reduce_kernel(const NormArgs g)
+// dw and db from the slices' sums, [groups][parts][2][pitch].  A block takes 32
+// neighbouring columns; its 16 warps take every 16th slice each, and the warps' sums
+// are added in order.
+__global__ void __launch_bounds__(512) norm_reduce_kernel(const NormArgs g, int pitch)
 {
     __shared__ float part[16][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int cols = 2 * g.d, per = (cols + 31) / 32;
-    const int64_t gi = blockIdx.x / static_cast<unsigned>(per);
-    const int col = static_cast<int>(blockIdx.x % static_cast<unsigned>(per)) * 32 + lane;
+    const int per = (g.d + 31) / 32;
+    const int64_t gi = blockIdx.x / static_cast<unsigned>(2 * per);
+    const int b = static_cast<int>(blockIdx.x % static_cast<unsigned>(2 * per));
+    const int which = b >= per, col = (b - which * per) * 32 + lane;
+    float *out = which ? g.dbias : g.dweight;
+    if (out == nullptr) return;
     grid_dependency_wait();
     float s = 0.f;
-    if (col < cols) {
-        const float *w = g.work + gi * g.parts * cols + col;
-#pragma unroll 8
-        for (int p = warp; p < g.parts; p += 16) s += w[static_cast<int64_t>(p) * cols];
+    if (col < g.d) {
+        const float *w = g.work + (gi * g.parts * 2 + which) * pitch + col;
+#pragma unroll 10
+        for (int p = warp; p < g.parts; p += 16) s += w[static_cast<int64_t>(p) * 2 * pitch];
     }
     part[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && col < cols) {
+    if (warp == 0 && col < g.d) {
         s = part[0][lane];
 #pragma unroll
         for (int k = 1; k < 16; ++k) s += part[k][lane];
-        float *out = col < g.d ? g.dweight : g.dbias;
-        if (out) out[gi * g.d + (col < g.d ? col : col - g.d)] = s;
+        out[gi * g.d + col] = s;
     }
 }
 
@@ -608,15 +680,15 @@ constexpr int kSmemMost = 224 * 1024;
 
 // A kernel's setup and the stages of its ring: 4, 2 or 1, as many as fit the share
 // of shared memory of a block where an SM holds 512 threads.
-template <int FMT, int TPR, typename Kernel>
+template <int FMT, typename T, typename Kernel>
 kq_status ring_setup(Kernel kern, DeviceOnce &once, NormArgs &g, int rows_per_stage, int &stage)
 {
     const kq_status st = once.run([&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
     });
-    constexpr int kResident = std::max(1, 512 / Team<TPR>::kThreads);
+    constexpr int kResident = std::max(1, 512 / T::kThreads);
     const int nc = (g.d + Chunk<FMT>::kN - 1) / Chunk<FMT>::kN;
-    stage = Team<TPR>::kPerBlock * rows_per_stage * 16 * nc;
+    stage = T::kPerBlock * rows_per_stage * 16 * nc;
     const int fit = kSmemMost / kResident / stage;
     g.stages = fit >= kMaxStages ? kMaxStages : fit >= 2 ? 2 : 1;
     return st;
@@ -625,11 +697,12 @@ kq_status ring_setup(Kernel kern, DeviceOnce &once, NormArgs &g, int rows_per_st
 template <int FMT, int TPR, int VPT, bool RAG>
 kq_status forward_t(NormArgs &g, cudaStream_t stream)
 {
-    constexpr int PB = Team<TPR>::kPerBlock, kResident = std::max(1, 512 / Team<TPR>::kThreads);
+    using T = FwdTeam<TPR>;
+    constexpr int PB = T::kPerBlock, kResident = std::max(1, 512 / T::kThreads);
     auto kern = norm_forward_kernel<FMT, TPR, VPT, RAG>;
     static DeviceOnce once;
     int stage;
-    const kq_status st = ring_setup<FMT, TPR>(kern, once, g, 1, stage);
+    const kq_status st = ring_setup<FMT, T>(kern, once, g, 1, stage);
     if (st != KQ_OK) return st;
     // one wave of teams, an even number of rows each (rows go two at a time; the
     // longest row leaves room for two)
@@ -638,7 +711,7 @@ kq_status forward_t(NormArgs &g, cudaStream_t stream)
     if (run > 1) run += run & 1;
     g.run = static_cast<int>(run);
     const int64_t blocks = (g.m + run * PB - 1) / (run * PB);
-    return launch_pdl(kern, static_cast<int>(blocks), Team<TPR>::kThreads,
+    return launch_pdl(kern, static_cast<int>(blocks), T::kThreads,
                       static_cast<size_t>(g.stages * stage), stream, g);
 }
 
@@ -658,23 +731,23 @@ kq_status forward_f(NormArgs &g, cudaStream_t stream)
     return KQ_ERR_SHAPE;
 }
 
-// Row slices per group of the backward pass: four blocks of 128 threads for
-// each of the 152 SMs in all, fewer where rows are few.
-constexpr int64_t kNormParts = 608;
+// Row slices per group of the backward pass: one block for each of the 152 SMs in
+// all, fewer where rows are few.
+constexpr int64_t kNormParts = 152;
 
 template <int FMT, int TPR, int VPT, bool RAG>
 kq_status backward_t(NormArgs &g, int64_t groups, cudaStream_t stream)
 {
-    constexpr int PB = Team<TPR>::kPerBlock, kResident = std::max(1, 512 / Team<TPR>::kThreads);
+    using T = BwdTeam<TPR>;
     auto kern = norm_backward_kernel<FMT, TPR, VPT, RAG>;
     static DeviceOnce once;
     int stage;
-    const kq_status st = ring_setup<FMT, TPR>(kern, once, g, 2, stage);
+    const kq_status st = ring_setup<FMT, T>(kern, once, g, 2, stage);
     if (st != KQ_OK) return st;
-    g.parts = static_cast<int>(
-        std::min<int64_t>(g.parts, std::max<int64_t>(1, kResident * 152 / groups)));
-    const int sums = PB > 1 ? 2 * static_cast<int>(sizeof(float)) * g.d : 0;
-    return launch_pdl(kern, static_cast<int>(groups * g.parts), Team<TPR>::kThreads,
+    constexpr int N = Chunk<FMT>::kN;
+    const int pitch = (g.d + N - 1) / N * N;
+    const int sums = T::kPerBlock / 2 * 2 * pitch * static_cast<int>(sizeof(float));
+    return launch_pdl(kern, static_cast<int>(groups * g.parts), T::kThreads,
                       static_cast<size_t>(std::max(g.stages * stage, sums)), stream, g);
 }
 
@@ -698,7 +771,7 @@ int64_t norm_parts(int64_t m, int64_t group_rows)
 {
     const int64_t groups = (m + group_rows - 1) / group_rows;
     const int64_t rows = std::min(m, group_rows);
-    return std::max<int64_t>(1, std::min((kNormParts + groups - 1) / groups, (rows + 3) / 4));
+    return std::max<int64_t>(1, std::min(kNormParts / groups, (rows + 7) / 8));
 }
 
 kq_status launch_norm_forward(const void *x, int64_t ldx, kq_format fmt, int64_t m, int64_t d,
@@ -767,8 +840,10 @@ kq_status launch_norm_backward(const void *dy, int64_t lddy, const void *x, int6
     else
         st = rag ? backward_f<KQ_F32, true>(g, groups, stream) : backward_f<KQ_F32, false>(g, groups, stream);
     if (st != KQ_OK || g.parts == 1 || (dweight == nullptr && dbias == nullptr)) return st;
-    const int64_t blocks = groups * ((2 * d + 31) / 32);
-    return launch_pdl(norm_reduce_kernel, static_cast<int>(blocks), 512, 0, stream, g);
+    const int chunk = static_cast<int>(16 / size);
+    const int pitch = static_cast<int>((d + chunk - 1) / chunk * chunk);
+    const int64_t blocks = groups * 2 * ((d + 31) / 32);
+    return launch_pdl(norm_reduce_kernel, static_cast<int>(blocks), 512, 0, stream, g, pitch);
 }
 
 }  // namespace kq
