@@ -417,6 +417,9 @@ KQ_API kq_status kq_linear(const void *a, int64_t lda, const void *w, int64_t ld
  *   tq, tk           rows of q and out, of k and v (< 2^31 - 1024)
  *   heads, kv_heads  heads % kv_heads == 0, heads <= 65536
  *   d                8 <= d <= 128, d % 8 == 0
+ *   max_k            an upper bound of the key lengths; it chooses the schedule
+ *                    (and the workspace): a wrong value costs speed, not
+ *                    correctness
  *   causal           0 or 1
  *   scale            > 0, finite (usually 1 / sqrt(d))
  *   out              device, fmt, strides as q's (written; not q, k or v)
@@ -432,12 +435,13 @@ KQ_API kq_status kq_attention(const void *q, int64_t q_token, int64_t q_head, co
                               int64_t k_token, int64_t k_head, const void *v, int64_t v_token,
                               int64_t v_head, kq_format fmt, const int32_t *cu_q, const int32_t *cu_k,
                               int64_t nseq, int64_t tq, int64_t tk, int64_t heads, int64_t kv_heads,
-                              int64_t d, int causal, float scale, void *out,
+                              int64_t d, int64_t max_k, int causal, float scale, void *out,
                               int64_t out_token, int64_t out_head, float *lse, void *workspace,
                               cudaStream_t stream);
 
 /* Workspace bytes of kq_attention (0 if none, or if the arguments are invalid). */
-KQ_API size_t kq_attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d);
+KQ_API size_t kq_attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d,
+                                 int64_t max_k);
 
 /*
  * kq_expand_blocks -- [KQ] Sec. 3.5.1 K1 (the dense 32x32 blocks are kept

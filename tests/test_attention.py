@@ -156,8 +156,9 @@ def test_whole_items_on_every_sm(causal):
 @gpu
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("heads,kv_heads,lq,lk", [
-    (2, 2, [2000, 300, 0, 1500], [2000, 700, 9, 1500]),     # shares of tile pairs
-    (8, 2, [1000, 1, 129], [3000, 2500, 129]),
+    (2, 2, [2000, 300, 0, 1500], [2000, 700, 9, 1500]),
+    (2, 2, [9000], [9000]),                                 # shares of tile pairs
+    (8, 2, [1000, 1, 129], [3000, 12500, 129]),
     (24, 24, [700], [700]),
     (1, 1, [2050], [2050])])
 def test_shares_of_tile_pairs(heads, kv_heads, lq, lk, causal):
@@ -254,8 +255,10 @@ def test_empty_bounds_stream_and_repeatable():
     lq, lk = [1, 4, 300], [3000, 90, 300]
     q, k, v = make(lq, lk, 8, 2, 128, torch.bfloat16, 11)
     first, _ = run(lq, lk, 8, 2, 128, torch.bfloat16, True, seed=11)
-    # the bounds of the lengths are not used: wrong ones change nothing
-    assert torch.equal(first, kq.kq_attention(q, k, v, offsets(lq), offsets(lk), 1, 1))
+    # a wrong bound of the key lengths changes the schedule only
+    for max_k in (None, 1, 10 ** 6):
+        out, lse = kq.kq_attention(q, k, v, offsets(lq), offsets(lk), 1, max_k, lse=True)
+        check(out, lse, q, k, v, lq, lk, True)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
@@ -278,17 +281,17 @@ FAKE = 1 << 20
 
 
 def _att(q=FAKE, qs=(256, 64), k=FAKE, ks=(128, 64), v=FAKE, vs=(128, 64), fmt=0, cu_q=FAKE, cu_k=FAKE,
-         nseq=2, tq=8, tk=8, heads=4, kv=2, d=64, causal=1, scale=0.125, out=FAKE, os=(256, 64),
+         nseq=2, tq=8, tk=8, heads=4, kv=2, d=64, max_k=4096, causal=1, scale=0.125, out=FAKE, os=(256, 64),
          lse=None, work=FAKE):
     return kq.lib().kq_attention(q, *qs, k, *ks, v, *vs, fmt, cu_q, cu_k, nseq, tq, tk, heads, kv, d,
-                                 causal, scale, out, *os, lse, work, None)
+                                 max_k, causal, scale, out, *os, lse, work, None)
 
 
 def test_argument_checks():
     assert _att(fmt=2) == 4 and _att(fmt=-1) == 4
     assert _att(d=60) == 2 and _att(d=0) == 2 and _att(d=136) == 2 and _att(heads=3) == 2
     assert _att(kv=0) == 2 and _att(tq=-1) == 2 and _att(tk=-1) == 2 and _att(nseq=-1) == 2
-    assert _att(tq=1 << 31) == 2 and _att(heads=1 << 17, kv=1 << 16) == 2
+    assert _att(max_k=-1) == 2 and _att(tq=1 << 31) == 2 and _att(heads=1 << 17, kv=1 << 16) == 2
     assert _att(scale=0.0) == 2 and _att(scale=-1.0) == 2 and _att(scale=float("nan")) == 2
     assert _att(scale=float("inf")) == 2
     assert _att(qs=(256, 32)) == 2 and _att(ks=(32, 64)) == 2 and _att(os=(0, 64)) == 2
@@ -302,9 +305,11 @@ def test_argument_checks():
 
 def test_workspace_bytes():
     size = kq.lib().kq_attention_bytes
-    assert size(0, 2, 4, 2, 64) == 0 and size(8, 2, 4, 3, 64) == 0 and size(8, 2, 4, 2, 60) == 0
-    assert size(8, 8, 32, 8, 128) > 0                        # few items: split
-    assert size(16384, 1, 24, 24, 128) == 0                  # whole items fill the SMs
+    assert size(0, 2, 4, 2, 64, 4096) == 0 and size(8, 2, 4, 3, 64, 4096) == 0
+    assert size(8, 2, 4, 2, 60, 4096) == 0
+    assert size(8, 8, 32, 8, 128, 4096) > 0                  # few items: split
+    assert size(8, 8, 32, 8, 128, 100) == 0                  # short keys: whole items
+    assert size(16384, 1, 24, 24, 128, 16384) == 0           # whole items fill the SMs
 
 
 def test_binding_refusals():

@@ -286,7 +286,7 @@ def test_backward_workspace_bytes():
     assert size(1, 64, 0) == 0 and size(0, 64, 0) == 0 and size(-1, 64, 0) == 0
     assert size(4, 0, 0) == 0 and size(4, 64, 1) == 0
     # at most 152 slices and one more per group, two fp32 rows of whole chunks each
-    for m, d, group in ((4096, 1152, 0), (65536, 1150, 4096), (1000, 96, 9)):
+    for m, d, group in ((4096, 1152, 0), (65536, 1150, 4096), (1000, 96, 100)):
         groups = 1 if group == 0 else -(-m // group)
         row = (d + 7) // 8 * 8
         assert 0 < size(m, d, group) <= (152 + groups) * 2 * row * 4

@@ -107,23 +107,6 @@ kq_status make_tensor_map_2d_f32(CUtensorMap *map, void *base, int64_t rows, int
     return r == CUDA_SUCCESS ? KQ_OK : KQ_ERR_CUDA;
 }
 
-kq_status make_tensor_map_3d_16(CUtensorMap *map, const void *base, int64_t d0, int64_t d1, int64_t d2,
-                                int64_t stride1, int64_t stride2, uint32_t box0, uint32_t box1,
-                                uint32_t box2)
-{
-    auto fn = encode_fn();
-    if (fn == nullptr) return KQ_ERR_CUDA;
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
-                                static_cast<cuuint64_t>(d2)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride1) * 2, static_cast<cuuint64_t>(stride2) * 2};
-    const cuuint32_t box[3] = {box0, box1, box2};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
-                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? KQ_OK : KQ_ERR_CUDA;
-}
-
 // ---------------------------------------------------------------------------
 // argument checks (host only; nothing is enqueued when they fail)
 

@@ -32,21 +32,23 @@
 // Schedule: persistent CTAs.  With many items (tile pair x key/value head), a CTA
 // takes whole items: the last tile pairs of all sequences first, then the ones
 // before them, ..., in rounds of alternating direction, so that lengths even out.
-// With fewer items than SMs, all items' key tiles are laid end to end and cut into
-// equal shares; an item cut by a share's border leaves normalised parts and their
+// With fewer items than SMs and long sequences, all items' key tiles are laid end to
+// end and cut into equal shares; an item cut by a share's border leaves normalised parts and their
 // lse in the workspace, and a second kernel joins them.  When even single tiles are
 // fewer than SMs (one new token per sequence), items are single tiles and the two
 // warpgroups take alternate key tiles of the same queries: the chain of product,
 // softmax and product takes longer than a key tile's way from HBM, and two chains
 // hide it.  Each warpgroup then leaves a part.
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <mutex>
 
+#include "kq_block.h"
 #include "kq_device.cuh"
 #include "kq_epilogue.cuh"
-#include "kq_internal.h"
 #include "kq_tcgen05.cuh"
 
 namespace kq {
@@ -495,6 +497,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         }
+        if (g.split) grid_dependents_launch();           // the join may be scheduled
         if (lane == 0) {
             // no copy is in flight when the CTA leaves
             for (int t = 0; t < 2; ++t)
@@ -944,6 +947,35 @@ kq_status launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorM
     return launch_pdl(attention_join_kernel<F16>, static_cast<int>((rows + 7) / 8), 256, 0, stream, g, grid);
 }
 
+// [d2][d1][d0] 16-bit elements (strides of d1 and d2 in elements), boxes with rows of
+// 128 bytes in the 128-byte swizzle.  (The driver entry point comes through the
+// runtime, as for the other maps.)
+kq_status make_tensor_map_3d_16(CUtensorMap *map, const void *base, int64_t d0, int64_t d1, int64_t d2,
+                                int64_t stride1, int64_t stride2, uint32_t box0, uint32_t box1,
+                                uint32_t box2)
+{
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    if (fn == nullptr) return KQ_ERR_CUDA;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1),
+                                static_cast<cuuint64_t>(d2)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride1) * 2, static_cast<cuuint64_t>(stride2) * 2};
+    const cuuint32_t box[3] = {box0, box1, box2};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides,
+                    box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? KQ_OK : KQ_ERR_CUDA;
+}
+
 // Query heads per tile: the whole group, or for groups of more than 128 heads
 // its largest divisor that fits.
 int heads_per_tile(int group)
@@ -963,29 +995,35 @@ int64_t items_most(int64_t tq, int64_t nseq, int64_t span, int64_t units)
 }
 
 // Fewer items than SMs: shares of key tiles (split); fewer single tiles than SMs:
-// alternate key tiles as well (alt).  Parts are numbered below items + CTAs.
+// alternate key tiles as well (alt).  Parts are numbered below items + CTAs.  The
+// shares pay where the longest chain of key tiles (about 1.2 us each) takes longer
+// than the second kernel (about 4 us and 1 us for 1000 rows): for 8 sequences of one
+// token and 32 / 8 heads whole items take 10.1, 13.3 and 20.0 us at 256, 512 and 1024
+// keys, shares 12.3, 13.6 and 16.3; for two prompts of 1024 tokens and 8 heads whole
+// items take 17.1 us, shares 31.5.
 struct Schedule {
     int gp, tpt, units;
     bool split, alt;
     int64_t items;
-    Schedule(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads)
+    Schedule(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t max_k)
     {
         gp = heads_per_tile(static_cast<int>(heads / kv_heads));
         tpt = 128 / gp;
         units = static_cast<int>(heads / gp);
         const int64_t tiles = items_most(tq, nseq, tpt, units);
-        alt = tiles < kAMaxGrid;
+        const bool pays = 12 * ((max_k + 127) / 128) > 40 + tq * heads / 100;
+        alt = tiles < kAMaxGrid && pays;
         items = alt ? tiles : items_most(tq, nseq, 2 * tpt, units);
-        split = items < kAMaxGrid;
+        split = items < kAMaxGrid && pays;
     }
     int64_t slots() const { return split ? items + kAMaxGrid : 0; }
 };
 
 }  // namespace
 
-size_t attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d)
+size_t attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_k)
 {
-    const Schedule sch(tq, nseq, heads, kv_heads);
+    const Schedule sch(tq, nseq, heads, kv_heads, max_k);
     return static_cast<size_t>(sch.slots()) * kASlotRows * (static_cast<size_t>(d) + 1) * sizeof(float);
 }
 
@@ -994,7 +1032,7 @@ kq_status launch_attention(const AttentionCall &c, cudaStream_t stream)
     DeviceInfo info;
     kq_status st = device_info(info);
     if (st != KQ_OK) return st;
-    const Schedule sch(c.tq, c.nseq, c.heads, c.kv_heads);
+    const Schedule sch(c.tq, c.nseq, c.heads, c.kv_heads, c.max_k);
     AttnArgs g{};
     g.cu_q = c.cu_q;
     g.cu_k = c.cu_k;

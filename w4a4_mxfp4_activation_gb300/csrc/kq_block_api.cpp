@@ -2,7 +2,7 @@
 // (layer norm, linear layer, attention): the argument checks, which run before anything is enqueued.
 #include <cmath>
 
-#include "kq_internal.h"
+#include "kq_block.h"
 
 using namespace kq;
 
@@ -52,10 +52,11 @@ kq_status check_linear(const LinearCall &c)
 
 constexpr int64_t kMaxTokens = (1LL << 31) - 1024;   // tile starts stay within int32
 
-bool attention_shape_ok(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d)
+bool attention_shape_ok(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d, int64_t max_k)
 {
     return tq >= 0 && tq <= kMaxTokens && nseq >= 0 && nseq <= kMaxTokens && kv_heads > 0 &&
-           heads > 0 && heads <= 65536 && heads % kv_heads == 0 && d >= 8 && d <= 128 && d % 8 == 0;
+           heads > 0 && heads <= 65536 && heads % kv_heads == 0 && d >= 8 && d <= 128 && d % 8 == 0 &&
+           max_k >= 0;
 }
 
 // Element strides of [token][head][d] rows: 16-byte steps, below 2^39 bytes.
@@ -158,12 +159,12 @@ kq_status kq_linear(const void *a, int64_t lda, const void *w, int64_t ldw, kq_f
 kq_status kq_attention(const void *q, int64_t q_token, int64_t q_head, const void *k, int64_t k_token,
                        int64_t k_head, const void *v, int64_t v_token, int64_t v_head, kq_format fmt,
                        const int32_t *cu_q, const int32_t *cu_k, int64_t nseq, int64_t tq, int64_t tk,
-                       int64_t heads, int64_t kv_heads, int64_t d, int causal, float scale,
+                       int64_t heads, int64_t kv_heads, int64_t d, int64_t max_k, int causal, float scale,
                        void *out, int64_t out_token, int64_t out_head, float *lse, void *workspace,
                        cudaStream_t stream)
 {
     if (fmt != KQ_BF16 && fmt != KQ_F16) return KQ_ERR_LAYOUT;
-    if (!attention_shape_ok(tq, nseq, heads, kv_heads, d) || tk < 0 || tk > kMaxTokens ||
+    if (!attention_shape_ok(tq, nseq, heads, kv_heads, d, max_k) || tk < 0 || tk > kMaxTokens ||
         !(scale > 0.f) || !std::isfinite(scale))
         return KQ_ERR_SHAPE;
     if (!stride_ok(q_token, q_head, d) || !stride_ok(k_token, k_head, d) ||
@@ -173,7 +174,7 @@ kq_status kq_attention(const void *q, int64_t q_token, int64_t q_head, const voi
     if (q == nullptr || out == nullptr || cu_q == nullptr || cu_k == nullptr ||
         (tk > 0 && (k == nullptr || v == nullptr)))
         return KQ_ERR_NULL;
-    if (workspace == nullptr && kq_attention_bytes(tq, nseq, heads, kv_heads, d) != 0)
+    if (workspace == nullptr && kq_attention_bytes(tq, nseq, heads, kv_heads, d, max_k) != 0)
         return KQ_ERR_NULL;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace) ||
         !aligned4(lse) || !aligned4(cu_q) || !aligned4(cu_k) ||
@@ -181,14 +182,15 @@ kq_status kq_attention(const void *q, int64_t q_token, int64_t q_head, const voi
         return KQ_ERR_ALIGN;
     const AttentionCall c = {q,        k,    v,     q_token,  q_head,    k_token,  k_head,
                              v_token,  v_head, fmt == KQ_F16, cu_q, cu_k, nseq, tq, tk, heads, kv_heads,
-                             d,        causal != 0, scale, out, out_token, out_head, lse, workspace};
+                             d,        max_k, causal != 0, scale, out, out_token, out_head, lse, workspace};
     return launch_attention(c, stream);
 }
 
-size_t kq_attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d)
+size_t kq_attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d,
+                          int64_t max_k)
 {
-    if (!attention_shape_ok(tq, nseq, heads, kv_heads, d) || tq == 0 || nseq == 0) return 0;
-    return attention_bytes(tq, nseq, heads, kv_heads, d);
+    if (!attention_shape_ok(tq, nseq, heads, kv_heads, d, max_k) || tq == 0 || nseq == 0) return 0;
+    return attention_bytes(tq, nseq, heads, kv_heads, d, max_k);
 }
 
 }  // extern "C"

@@ -36,6 +36,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "kq_block.h"
 #include "kq_device.cuh"
 #include "kq_epilogue.cuh"
 #include "kq_internal.h"

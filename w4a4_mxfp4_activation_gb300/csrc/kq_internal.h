@@ -2,7 +2,6 @@
 #pragma once
 
 #include <cstdint>
-#include <mutex>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -58,26 +57,7 @@ kq_status make_tensor_map_2d_u8(CUtensorMap *map, void *base, int64_t rows, int6
 kq_status make_tensor_map_2d_f32(CUtensorMap *map, void *base, int64_t rows, int64_t cols,
                                  int64_t ld_elems, uint32_t box_cols, uint32_t box_rows,
                                  CUtensorMapSwizzle swizzle);
-// [d2][d1][d0] 16-bit elements (strides of d1 and d2 in elements), boxes with
-// rows of 128 bytes in the 128-byte swizzle.
-kq_status make_tensor_map_3d_16(CUtensorMap *map, const void *base, int64_t d0, int64_t d1, int64_t d2,
-                                int64_t stride1, int64_t stride2, uint32_t box0, uint32_t box1,
-                                uint32_t box2);
 kq_status check_launch();
-
-// Runs a kernel's one-time setup (cudaFuncSetAttribute) once per device.
-struct DeviceOnce {
-    std::once_flag once[64];
-    cudaError_t err[64] = {};
-    template <typename F>
-    kq_status run(F &&setup)
-    {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KQ_ERR_CUDA;
-        std::call_once(once[dev], [&] { err[dev] = setup(); });
-        return err[dev] == cudaSuccess ? KQ_OK : KQ_ERR_CUDA;
-    }
-};
 
 // The kernels walk tiles in 32-bit arithmetic: row and column tile indices,
 // and the walk's start and stride (at most twice the grid), must fit in int.
@@ -132,60 +112,6 @@ kq_status launch_bf16_gemm(const uint16_t *a, int64_t lda, const uint16_t *w, in
                            cudaStream_t stream);
 kq_status launch_layer_error(const float *c, int64_t ldc, const float *r, int64_t ldr, int64_t m,
                              int64_t n, double *out, cudaStream_t stream);
-
-// Layer norm; group_rows > 0.  norm_parts: row slices per group of the
-// backward pass (its workspace is [groups][parts][2][d rounded up] fp32 when parts > 1).
-int64_t norm_parts(int64_t m, int64_t group_rows);
-kq_status launch_norm_forward(const void *x, int64_t ldx, kq_format fmt, int64_t m, int64_t d,
-                              const float *weight, const float *bias, int64_t group_rows, float eps,
-                              void *y, int64_t ldy, float *mean, float *rstd, cudaStream_t stream);
-kq_status launch_norm_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
-                               kq_format fmt, int64_t m, int64_t d, const float *weight,
-                               int64_t group_rows, const float *mean, const float *rstd, void *dx,
-                               int64_t lddx, float *dweight, float *dbias, void *workspace,
-                               cudaStream_t stream);
-
-// A linear layer, out = residual + act(A W^T + bias).  mx: a and w are packed
-// MXFP4 codes (pitches in bytes) with their tiled scales, else 16-bit rows in
-// fmt_in (pitches in elements); residual and out are in fmt_out.
-struct LinearCall {
-    bool mx;
-    const void *a;
-    int64_t lda;
-    const uint8_t *sfa;
-    const void *w;
-    int64_t ldw;
-    const uint8_t *sfw;
-    int fmt_in;
-    int64_t m, n, k;
-    const float *bias;
-    int act;
-    const void *residual;
-    int64_t ldr;
-    void *out;
-    int64_t ldo;
-    int fmt_out;
-};
-kq_status launch_linear(const LinearCall &c, cudaStream_t stream);
-kq_status launch_linear_tiles(const LinearCall &c, cudaStream_t stream);   // the products' kernel
-
-// Attention over packed sequences; strides in elements.  attention_bytes: its
-// workspace (0 where no item is split).
-struct AttentionCall {
-    const void *q, *k, *v;
-    int64_t q_token, q_head, k_token, k_head, v_token, v_head;
-    bool f16;
-    const int32_t *cu_q, *cu_k;
-    int64_t nseq, tq, tk, heads, kv_heads, d;
-    bool causal;
-    float scale;
-    void *out;
-    int64_t out_token, out_head;
-    float *lse;
-    void *workspace;
-};
-size_t attention_bytes(int64_t tq, int64_t nseq, int64_t heads, int64_t kv_heads, int64_t d);
-kq_status launch_attention(const AttentionCall &c, cudaStream_t stream);
 
 kq_status validate_quant_args(const uint16_t *A, int64_t m, int64_t d, int64_t lda,
                               const uint8_t *q, int64_t ldq, const uint8_t *sf,

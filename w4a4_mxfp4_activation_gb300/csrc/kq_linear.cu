@@ -14,9 +14,9 @@
 #include <algorithm>
 #include <mutex>
 
+#include "kq_block.h"
 #include "kq_device.cuh"
 #include "kq_epilogue.cuh"
-#include "kq_internal.h"
 #include "kq_tcgen05.cuh"
 
 namespace kq {

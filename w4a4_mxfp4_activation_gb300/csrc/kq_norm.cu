@@ -22,8 +22,8 @@
 
 #include <algorithm>
 
+#include "kq_block.h"
 #include "kq_device.cuh"
-#include "kq_internal.h"
 
 namespace kq {
 namespace {

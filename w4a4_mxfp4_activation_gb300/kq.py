@@ -135,9 +135,9 @@ def lib() -> ctypes.CDLL:
                                     vp]
             L.kq_linear.restype = st
             L.kq_attention.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i64, st, vp, vp, i64, i64,
-                                       i64, i64, i64, i64, st, f32, vp, i64, i64, vp, vp, vp]
+                                       i64, i64, i64, i64, i64, st, f32, vp, i64, i64, vp, vp, vp]
             L.kq_attention.restype = st
-            L.kq_attention_bytes.argtypes = [i64, i64, i64, i64, i64]
+            L.kq_attention_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
             L.kq_attention_bytes.restype = ctypes.c_size_t
             _lib = L
     return _lib
@@ -667,8 +667,9 @@ def kq_attention(q, k, v, cu_q, cu_k, max_q: int | None = None, max_k: int | Non
     """Attention over packed sequences: q [tq, heads, d], k and v [tk, kv_heads,
     d] (bfloat16 or float16, any strides that are multiples of 8 elements),
     sequence b in rows cu_q[b]..cu_q[b + 1] of q and cu_k[b]..cu_k[b + 1] of k and
-    v (int32 [nseq + 1]).  The bounds of the lengths, max_q and max_k, that callers
-    often carry along are not needed and not used; scale defaults to 1 / sqrt(d).
+    v (int32 [nseq + 1]).  max_k bounds the key lengths; it chooses the schedule, and
+    without it (None) they are taken as long.  (max_q, which callers carry along, is
+    not needed.)  scale defaults to 1 / sqrt(d).
     Returns out [tq, heads, d], or (out, lse [tq, heads] fp32) with ``lse=True``."""
     torch = _torch or _load_torch()
     q_token, q_head = _heads(q, "q")
@@ -690,11 +691,13 @@ def kq_attention(q, k, v, cu_q, cu_k, max_q: int | None = None, max_k: int | Non
         o_token, o_head = _heads(out, "out")
     stats = torch.empty((tq, heads), dtype=torch.float32, device=device) if lse else None
     L = _lib or lib()
-    nbytes = L.kq_attention_bytes(tq, nseq, heads, kv_heads, d)
+    if max_k is None:
+        max_k = tk
+    nbytes = L.kq_attention_bytes(tq, nseq, heads, kv_heads, d, max_k)
     work = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     _check(L.kq_attention(q.data_ptr(), q_token, q_head, k.data_ptr(), *_heads(k, "k"),
                           v.data_ptr(), *_heads(v, "v"), fmt, cu_q.data_ptr(), cu_k.data_ptr(), nseq,
-                          tq, tk, heads, kv_heads, d, 1 if causal else 0,
+                          tq, tk, heads, kv_heads, d, max_k, 1 if causal else 0,
                           d ** -0.5 if scale is None else scale, out.data_ptr(), o_token, o_head,
                           stats.data_ptr() if lse else None, work.data_ptr() if nbytes else None,
                           _handle(stream, device)),
