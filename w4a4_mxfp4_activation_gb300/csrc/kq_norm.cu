@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(FwdTeam<TPR>::kThreads, 512 / FwdTeam<TPR>::kT
     if (t == 0)
         for (int i = 0; i < S; ++i) fill(i);
     bool dead = false;                                      // a copy did not arrive in time
+    const bool plain = g.weight != nullptr && g.bias != nullptr && g.vec;
     // the group of the current row, and how many of its rows are left
     int64_t grp = first / g.group_rows, left = (grp + 1) * g.group_rows - first;
 #pragma unroll 1
@@ -393,28 +394,54 @@ __global__ void __launch_bounds__(FwdTeam<TPR>::kThreads, 512 / FwdTeam<TPR>::kT
         // rsqrtf is within 2 ulp, and its few instructions run in every thread
         float rstd[2] = {rsqrtf(var.x * g.inv_d + g.eps), rsqrtf(var.y * g.inv_d + g.eps)};
         if (dead) rstd[0] = rstd[1] = __uint_as_float(kNan);
-        const bool same = left > 1;
         const float *w = g.weight ? g.weight + grp * g.d : nullptr;
         const float *b = g.bias ? g.bias + grp * g.d : nullptr;
-        uint8_t *yr = g.y + (first + i) * g.ypitch;
+        uint8_t *yr = g.y + (first + i) * g.ypitch + 16 * t;
+        if (!RAG && plain && two && left > 1) {
+            // both rows of one group, whole chunks, aligned parameters: no tests
+            const float4 *wp = reinterpret_cast<const float4 *>(w + t * N);
+            const float4 *bp = reinterpret_cast<const float4 *>(b + t * N);
+            uint8_t *y1 = yr + g.ypitch;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int c = t + k * TPR;
-            if (c < nc) {
-                float2 wv[P], bv[P];
-                load_param<P>(w, c, g.d, g.vec, 1.f, wv);
-                load_param<P>(b, c, g.d, g.vec, 0.f, bv);
+            for (int k = 0; k < VPT; ++k) {
+                if (t + k * TPR < nc) {
+                    float2 wv[P], bv[P];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    if (r == 1 && !two) break;
-                    if (r == 1 && !same) {
-                        load_param<P>(w ? w + g.d : nullptr, c, g.d, g.vec, 1.f, wv);
-                        load_param<P>(b ? b + g.d : nullptr, c, g.d, g.vec, 0.f, bv);
+                    for (int j = 0; j < P; j += 2) {
+                        const float4 f = __ldg(wp + (k * TPR * N + 2 * j) / 4);
+                        const float4 h = __ldg(bp + (k * TPR * N + 2 * j) / 4);
+                        wv[j] = make_float2(f.x, f.y);
+                        wv[j + 1] = make_float2(f.z, f.w);
+                        bv[j] = make_float2(h.x, h.y);
+                        bv[j + 1] = make_float2(h.z, h.w);
                     }
 #pragma unroll
-                    for (int j = 0; j < P; ++j)
-                        v[r][k][j] = __ffma2_rn(__fmul2_rn(v[r][k][j], both(rstd[r])), wv[j], bv[j]);
-                    store_chunk<FMT, RAG>(yr + r * g.ypitch, c, g.d, pack<FMT>(v[r][k]));
+                    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                        for (int j = 0; j < P; ++j)
+                            v[r][k][j] = __ffma2_rn(__fmul2_rn(v[r][k][j], both(rstd[r])), wv[j], bv[j]);
+                        stg128_cs((r ? y1 : yr) + 16 * TPR * k, pack<FMT>(v[r][k]));
+                    }
+                }
+            }
+        } else {
+            // (the second row may be missing, or belong to the next group)
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int c = t + k * TPR;
+                if (c < nc) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if (r == 1 && !two) break;
+                        const int64_t next = r == 1 && left <= 1 ? g.d : 0;
+                        float2 wv[P], bv[P];
+                        load_param<P>(w ? w + next : nullptr, c, g.d, g.vec, 1.f, wv);
+                        load_param<P>(b ? b + next : nullptr, c, g.d, g.vec, 0.f, bv);
+#pragma unroll
+                        for (int j = 0; j < P; ++j)
+                            v[r][k][j] = __ffma2_rn(__fmul2_rn(v[r][k][j], both(rstd[r])), wv[j], bv[j]);
+                        store_chunk<FMT, RAG>(yr + r * g.ypitch - 16 * t, c, g.d, pack<FMT>(v[r][k]));
+                    }
                 }
             }
         }
