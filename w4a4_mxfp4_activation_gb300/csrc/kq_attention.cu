@@ -20,8 +20,9 @@
 // token's heads share one read of the cache and causal tiles waste little.
 //
 // Roles: warps 0-3 and 4-7 softmax of tile 0 and 1 (thread = row), warp 8
-// schedule and TMA loads, warp 9 the MMAs (10 and 11 only give their registers
-// away).  Issuing an MMA costs its warp about as long as the tensor cores take for
+// schedule and TMA loads, warp 9 the MMAs, warps 10 and 11 the TMA stores of the
+// output tiles, which the softmax warps leave in shared memory (stored by themselves,
+// 32 KB kept a warpgroup from its next tile for 2800 cycles).  Issuing an MMA costs its warp about as long as the tensor cores take for
 // it, hence straight-line code on warp-uniform operands.  (A warp of its own for each
 // tile's MMAs was slower: 1223 against 1106 us on the 16384-token prompt.)
 // TMEM: scores of the tiles at columns 0 and 128 (P, 16-bit, over the first half
@@ -344,12 +345,22 @@ __device__ __forceinline__ void store_row(uint8_t *dst, const uint32_t (&o)[32],
         if (4 * k < left) stg256(dst + 4 * k, o + k);
 }
 
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *map, int32_t x, int32_t y, int32_t z,
+                                             uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+
 // ---- the kernel ------------------------------------------------------------------------
 
 template <int DA, bool F16>
 __global__ void __launch_bounds__(kAThreads, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const AttnArgs g)
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                     const AttnArgs g)
 {
     using C = ACfg<DA>;
     extern __shared__ uint8_t smem_raw[];
@@ -361,14 +372,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
     const uint32_t b1 = bar + 16 * C::kStages;
     // per tile: Q, scores, P (in halves), O; then the two segment buffers
     const uint32_t q_full = b1, q_empty = b1 + 16, s_full = b1 + 32, p_ready = b1 + 48, o_full = b1 + 80;
-    const uint32_t drain = b1 + 96, seg_full = b1 + 112, seg_empty = b1 + 128;
-    const uint32_t tmem_slot = b1 + 144;
+    const uint32_t drain = b1 + 96, seg_full = b1 + 112, seg_empty = b1 + 128, staged = b1 + 144;
+    const uint32_t tmem_slot = b1 + 160;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
+        tma_prefetch_desc(&tmO);
         for (int s = 0; s < C::kStages; ++s) {
             mbar_init(kv_full + 8 * s, 1);
             mbar_init(kv_empty + 8 * s, 1);
@@ -382,7 +394,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
             mbar_init(o_full + 8 * q, 1);
             mbar_init(drain + 8 * q, 1);
             mbar_init(seg_full + 8 * q, 1);
-            mbar_init(seg_empty + 8 * q, 9);             // MMA and softmax warps
+            mbar_init(seg_empty + 8 * q, 11);            // all warps but the scheduler
+            mbar_init(staged + 8 * q, 4);                // the softmax warps
         }
         mbar_fence_init();
     }
@@ -639,8 +652,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 }
                 continue;
             }
-            // The stages of tile 0's last K and tile 1's last V are released by their
-            // softmax warps when the output is written: it passes through them.
+            // The stages of tile 0's last K and tile 1's last V are released by the
+            // output warps when the output is written: it passes through them.
             wait(kv_full + 8 * st, par);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -688,7 +701,36 @@ __global__ void __launch_bounds__(kAThreads, 1)
         __syncwarp();
         (void)mbar_wait(drain, 0);
     } else if (warp >= 10) {
+        // Output tile t, from the stage that its softmax warps filled: one TMA store
+        // per 64 channels.  A store clips at the last row of the output, not of the
+        // sequence: tiles with fewer tokens are left to the softmax warps.
         regs_dec<kARegsOther>();
+        const int t = warp - 10;
+        int kbase = 0;
+        uint32_t par = 0;
+        bool ok = true;
+        for (int i = 0; ok && take(i); ++i) {
+            const Segment &s = segs[i & 1];
+            const int n0 = tiles_of(g, s, 0), n1 = tiles_of(g, s, 1), n = t ? n1 : n0;
+            const int stage = (kbase + 2 * (n - 1) + t + C::kStages) % C::kStages;
+            kbase = (kbase + 2 * (g.alt ? n0 + n1 : max(n0, n1))) % C::kStages;
+            const int first = s.t0 + t * g.tpt, row = s.q0 + first, head = s.unit * g.gp;
+            const bool mine = n > 0 && s.slot < 0 && first + g.tpt <= s.qlen;
+            give_back(i);
+            if (!mine) continue;
+            ok = __all_sync(0xffffffffu, mbar_wait(staged + 8 * t, par));
+            par ^= 1;
+            if (ok && lane == 0) {
+                const uint32_t box = ring + static_cast<uint32_t>(stage) * C::kTile;
+                for (int a = 0; a < DA; ++a) tma_store_3d(&tmO, 64 * a, head, row, box + a * kABoxBytes);
+                bulk_commit_group();
+                bulk_wait_group_read<0>();
+                mbar_arrive(kv_empty + 8 * stage);
+            }
+            __syncwarp();
+        }
+        if (lane == 0) bulk_wait_group_all();
+        __syncwarp();
     } else {
         regs_inc<kARegsSoftmax>();
         const int t = warp >> 2, qtr = warp & 3;
@@ -823,28 +865,37 @@ __global__ void __launch_bounds__(kAThreads, 1)
                         *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(g.out) + at + 16 * c) = make_uint4(0, 0, 0, 0);
                 continue;
             }
-            // Through shared memory, so that a store instruction writes whole rows
-            // and not 16 bytes of each of 32: the stage of the tile's last K (tile
-            // 0; every product with it is done) or V (tile 1), 32 rows a warp.
-            const uint32_t box = ring + static_cast<uint32_t>(stage) * C::kTile + qtr * 32 * DA * 128;
-            const uint32_t mine = box + lane * DA * 128;
+            // Into shared memory, in the layout of the output's TMA boxes: the stage of
+            // the tile's last K (tile 0; every product with it is done) or V (tile 1).
+            const uint32_t box = ring + static_cast<uint32_t>(stage) * C::kTile;
             for (int c = 0; c < g.d; c += 32) {
                 uint32_t o[32];
                 load_o(o, to + c, n, inv);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    sts128(mine + ((((c >> 3) + k) ^ (lane & 7)) << 4),
+                for (int k = 0; k < 4; ++k) {
+                    const int cc = (c >> 3) + k;
+                    sts128(box + (cc >> 3) * kABoxBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4),
                            make_uint4(pack16(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1]), F16),
                                       pack16(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3]), F16),
                                       pack16(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5]), F16),
                                       pack16(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7]), F16)));
+                }
             }
             g_fence_before();
+            if (first + g.tpt <= s.qlen) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(staged + 8 * t);
+                continue;
+            }
+            // a tile that ends with its sequence: rows by the warp, whole rows an
+            // instruction
             __syncwarp();
-            for (int c = lane; c < 32 * cpr; c += 32) {  // 32 rows of cpr chunks, in order
+            for (int c = lane; c < 32 * cpr; c += 32) {
                 const int rr = c / cpr, cc = c - rr * cpr;
                 const int64_t to_row = __shfl_sync(0xffffffffu, real ? at : int64_t(-1), rr);
-                const uint4 v = lds128(box + rr * DA * 128 + ((cc ^ (rr & 7)) << 4));
+                const uint4 v = lds128(box + (cc >> 3) * kABoxBytes + (qtr * 32 + rr) * 128 +
+                                       (((cc & 7) ^ (rr & 7)) << 4));
                 if (to_row >= 0) *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(g.out) + to_row + 16 * cc) = v;
             }
             fence_proxy_async_smem();
@@ -933,7 +984,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(const AttnArgs g, i
 
 template <int DA, bool F16>
 kq_status launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv,
-                   const AttnArgs &g, int grid, cudaStream_t stream)
+                   const CUtensorMap &mo, const AttnArgs &g, int grid, cudaStream_t stream)
 {
     auto kern = attention_kernel<DA, F16>;
     static DeviceOnce once;
@@ -941,7 +992,7 @@ kq_status launch_t(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorM
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ACfg<DA>::kSmem);
     });
     if (st != KQ_OK) return st;
-    st = launch_pdl(kern, grid, kAThreads, static_cast<size_t>(ACfg<DA>::kSmem), stream, mq, mk, mv, g);
+    st = launch_pdl(kern, grid, kAThreads, static_cast<size_t>(ACfg<DA>::kSmem), stream, mq, mk, mv, mo, g);
     if (st != KQ_OK || !g.split) return st;
     const int64_t rows = static_cast<int64_t>(g.tq) * g.heads;
     return launch_pdl(attention_join_kernel<F16>, static_cast<int>((rows + 7) / 8), 256, 0, stream, g, grid);
@@ -1057,7 +1108,7 @@ kq_status launch_attention(const AttentionCall &c, cudaStream_t stream)
     g.part = static_cast<float *>(c.workspace);
     g.slots = static_cast<int>(sch.slots());
     g.part_lse = g.part + sch.slots() * kASlotRows * g.d;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     st = make_tensor_map_3d_16(&mq, c.q, c.d, c.heads, c.tq, c.q_head, c.q_token, 64,
                                static_cast<uint32_t>(g.gp), static_cast<uint32_t>(g.tpt));
     // no keys at all: no tile is loaded, and the maps only have to be well formed
@@ -1067,14 +1118,17 @@ kq_status launch_attention(const AttentionCall &c, cudaStream_t stream)
         st = make_tensor_map_3d_16(&mk, kp, c.d, c.kv_heads, tk, c.k_head, c.k_token, 64, 1, 128);
     if (st == KQ_OK)
         st = make_tensor_map_3d_16(&mv, vp, c.d, c.kv_heads, tk, c.v_head, c.v_token, 64, 1, 128);
+    if (st == KQ_OK)
+        st = make_tensor_map_3d_16(&mo, c.out, c.d, c.heads, c.tq, c.out_head, c.out_token, 64,
+                                   static_cast<uint32_t>(g.gp), static_cast<uint32_t>(g.tpt));
     if (st != KQ_OK) return st;
     const int sms = std::min(info.sm_count, kAMaxGrid);
     const int grid = g.split ? sms : static_cast<int>(std::min<int64_t>(sch.items, sms));
     if (c.d <= 64)
-        return c.f16 ? launch_t<1, true>(mq, mk, mv, g, grid, stream)
-                     : launch_t<1, false>(mq, mk, mv, g, grid, stream);
-    return c.f16 ? launch_t<2, true>(mq, mk, mv, g, grid, stream)
-                 : launch_t<2, false>(mq, mk, mv, g, grid, stream);
+        return c.f16 ? launch_t<1, true>(mq, mk, mv, mo, g, grid, stream)
+                     : launch_t<1, false>(mq, mk, mv, mo, g, grid, stream);
+    return c.f16 ? launch_t<2, true>(mq, mk, mv, mo, g, grid, stream)
+                 : launch_t<2, false>(mq, mk, mv, mo, g, grid, stream);
 }
 
 }  // namespace kq
