@@ -502,7 +502,9 @@ def _empty_rows(m: int, n: int, dtype, fmt: int, device):
     if n % unit == 0:
         return _torch.empty((m, n), dtype=dtype, device=device), n
     ld = n + (-n) % unit
-    return _torch.empty((m, ld), dtype=dtype, device=device)[:, :n], ld
+    # (a strided allocation covers the last row up to column n only, which is all that
+    # is written; a slice of whole rows costs three times as much to make)
+    return _torch.empty_strided((m, n), (ld, 1), dtype=dtype, device=device), ld
 
 
 def _f32(t, what: str, *shape):
@@ -544,7 +546,9 @@ def kq_layer_norm(x, weight=None, bias=None, eps: float = 1e-6, group_rows: int 
         ldy = _rows(y, m, d, fmt, "y")
     mean = rstd = pm = pr = None
     if stats:
-        mean, rstd = torch.empty((2, m), dtype=torch.float32, device=device).unbind(0)
+        # (two allocations take half the time of one and its two views)
+        mean = torch.empty(m, dtype=torch.float32, device=device)
+        rstd = torch.empty(m, dtype=torch.float32, device=device)
         pm, pr = mean.data_ptr(), rstd.data_ptr()
     _check((_lib or lib()).kq_layer_norm(x.data_ptr(), ldx, fmt, m, d, w, b, group_rows, eps,
                                          y.data_ptr(), ldy, pm, pr, _handle(stream, device)),
@@ -573,7 +577,8 @@ def kq_layer_norm_backward(dy, x, weight, mean, rstd, group_rows: int = 0, dx=No
     else:
         lddx = _rows(dx, m, d, fmt, "dx")
     L = _lib or lib()
-    dweight, dbias = torch.empty((2, groups, d), dtype=torch.float32, device=device).unbind(0)
+    dweight = torch.empty((groups, d), dtype=torch.float32, device=device)
+    dbias = torch.empty((groups, d), dtype=torch.float32, device=device)
     nbytes = L.kq_layer_norm_backward_bytes(m, d, group_rows)
     work = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
     _check(L.kq_layer_norm_backward(dy.data_ptr(), lddy, x.data_ptr(), ldx, fmt, m, d, w,
