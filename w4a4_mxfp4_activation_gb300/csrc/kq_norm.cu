@@ -613,6 +613,7 @@ __global__ void __launch_bounds__(BwdTeam<TPR>::kThreads, 1)
         }
     }
     if (t == 0 && dead) ring.drain(rows, S);
+    grid_dependents_launch();                   // the second kernel may be scheduled
     if (g.dweight == nullptr && g.dbias == nullptr) return;
     // the teams' sums, halving their number: the upper half's go through shared
     // memory ([teams][2][pitch]); then the block's, in rows of whole chunks
