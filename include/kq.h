@@ -322,7 +322,8 @@ KQ_API kq_status kq_layer_error(const float *c, int64_t ldc, const float *c_ref,
  *   y, ldy      device, [m][ldy] in fmt (written, columns < d; not x)
  *   mean, rstd  device fp32 [m] or NULL: if given, receive the statistics
  * x, y, weight and bias are 16-byte aligned, and the row pitches of x and y
- * multiples of 16 bytes (ldx % 8 == 0 for 16-bit types, % 4 for fp32).
+ * multiples of 16 bytes (ldx % 8 == 0 for 16-bit types, % 4 for fp32).  A copy that
+ * stalls for about a second gives up, and its rows are NaN.
  */
 KQ_API kq_status kq_layer_norm(const void *x, int64_t ldx, kq_format fmt, int64_t m, int64_t d,
                                const float *weight, const float *bias, int64_t group_rows,
@@ -429,7 +430,9 @@ KQ_API kq_status kq_linear(const void *a, int64_t lda, const void *w, int64_t ld
  * Pointers are 16-byte aligned.  A NaN or infinity in k or v of one sequence
  * does not reach another.  Within a sequence a masked key has weight zero, and
  * zero times a non-finite v is NaN for the rows of the same tile, as in the
- * formula read literally.  The same inputs give the same bits.
+ * formula read literally.  The same inputs give the same bits.  A pipeline that
+ * stalls for about a second stops; the rows it had not finished are left as they
+ * were.
  */
 KQ_API kq_status kq_attention(const void *q, int64_t q_token, int64_t q_head, const void *k,
                               int64_t k_token, int64_t k_head, const void *v, int64_t v_token,

@@ -20,7 +20,8 @@
 //                                memory (exact: an MXFP4 element times its
 //                                power-of-two scale has at most two significant
 //                                bits) and multiplied with kind::f16;
-// and the fp64 error sums.  Every wait is bounded in time; a CTA that times
+// and the fp64 error sums.  The first two also carry the linear layers (bias,
+// activation, residual: LinearEpilogue).  Every wait is bounded in time; a CTA that times
 // out stops and leaves its remaining tiles unwritten, and the call reports
 // nothing (results are then undefined), as for the quantizers.
 //

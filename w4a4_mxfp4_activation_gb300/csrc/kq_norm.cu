@@ -16,7 +16,9 @@
 // works on a row (forward: on two) in registers, at most three 16-byte chunks a
 // thread for all but the longest rows.  While it does, bulk copies bring its
 // next rows into a ring in shared memory: loads into registers leave no room
-// for a second row, and an SM has to keep about 40 KB in flight.
+// for a second row, and an SM has to keep about 40 KB in flight.  Measured on GB300:
+// forward 65536 x 1152 bf16 56.9 us (5.3 TB/s), backward 18432 x 12288 bf16 204 us
+// (6.66 TB/s, 0.98 of the copy rate), 65536 x 3072 186 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
