@@ -766,8 +766,7 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
                 const uint32_t acc = tmem_base + (static_cast<uint32_t>(qtr * 32) << 16) +
                                      static_cast<uint32_t>(kXBN * b + C::kEpiCols * h);
                 Epilogue::run(g, ecol, erow, acc, acc_empty + 8 * b, resid);
-                continue;
-            }
+            } else {
             uint32_t v[128];
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(qtr * 32) << 16) + 128 * (b + h);
             asm volatile(
@@ -861,9 +860,12 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
                 for (int j = 0; j < 128; ++j)
                     if (x0 + j >= n4 && x0 + j < g.n) crow[j] = __uint_as_float(v[j]);
             }
+            }   // EPI == 0
         }
-        if (lane == 0) bulk_wait_group_all();   // the stores have read shared memory and landed
-        __syncwarp();
+        if constexpr (EPI == 0) {
+            if (lane == 0) bulk_wait_group_all();   // the stores have read shared memory and landed
+            __syncwarp();
+        }
     }
 
     g_fence_before();
