@@ -26,21 +26,33 @@ __device__ __forceinline__ float times_sigmoid2(float x, float t)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// x (1 + erf(x / sqrt 2)) / 2 = max(x, 0) - |x| q / 2 with q = erfc(|x| / sqrt 2), by
-// the rational approximation 7.1.26 of Abramowitz and Stegun, Handbook of
-// Mathematical Functions: erfc(a) = (a1 t + ... + a5 t^5) exp(-a^2), t = 1 / (1 + p a),
-// within 1.5e-7.  (erff took 1.3 times as long in the epilogue of short products.)
-// |x| is capped where q is zero, so that an infinity does not meet it.
-__device__ __forceinline__ float act_gelu(float x)
+__device__ __forceinline__ float max_nan(float a, float b)
 {
-    const float a = fabsf(x) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, a, 1.0f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    q = q * t * ex2_approx(a * a * -kLog2e);
-    return fmaf(-0.5f * fminf(fabsf(x), 64.0f), q, fmaxf(x, 0.0f));
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// x (1 + erf(x / sqrt 2)) / 2 = max(x, 0) - a q with a = |x| and q = erfc(a / sqrt 2) / 2
+// = 2^P(a), P a polynomial of degree 7 fitted to log2 q on [0, 6] (minimax in the
+// error of max(a, 1) q by linear programming: q and a q are within 1e-7).  a is
+// capped at 6, where a q is 6e-9.  Two elements at a time, in paired arithmetic, with one
+// special function and no division: 4096 x 4608 x 1152 25.4 us against 33.1 with a
+// rational form of erfc (one division, one exponential); 21.2 without an activation.
+// (One reciprocal for two elements of the other two activations changed nothing.)
+__device__ __forceinline__ float2 act_gelu2(float2 x)
+{
+    const float2 a = make_float2(fminf(fabsf(x.x), 6.0f), fminf(fabsf(x.y), 6.0f));
+    const auto both = [](float c) { return make_float2(c, c); };
+    float2 p = __ffma2_rn(both(6.119226782e-6f), a, both(-3.247830682e-5f));
+    p = __ffma2_rn(p, a, both(-4.947101697e-4f));
+    p = __ffma2_rn(p, a, both(7.508283015e-3f));
+    p = __ffma2_rn(p, a, both(-5.278469250e-2f));
+    p = __ffma2_rn(p, a, both(-4.591203034e-1f));
+    p = __ffma2_rn(p, a, both(-1.151114941f));
+    p = __ffma2_rn(p, a, both(-0.999999821f));
+    return make_float2(fmaf(-a.x, ex2_approx(p.x), max_nan(x.x, 0.0f)),
+                       fmaf(-a.y, ex2_approx(p.y), max_nan(x.y, 0.0f)));
 }
 __device__ __forceinline__ float act_gelu_tanh(float x)
 {
@@ -55,7 +67,11 @@ __device__ __forceinline__ void apply_act(float (&v)[N], int act)
 {
     if (act == KQ_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = act_gelu(v[i]);
+        for (int i = 0; i < N; i += 2) {
+            const float2 y = act_gelu2(make_float2(v[i], v[i + 1]));
+            v[i] = y.x;
+            v[i + 1] = y.y;
+        }
     } else if (act == KQ_ACT_GELU_TANH) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = act_gelu_tanh(v[i]);
