@@ -378,7 +378,9 @@ struct XCfg {
     static constexpr int kBoxBufs = EPI != 0 ? 0 : (NH == 1 ? 2 : 1);
     static constexpr int kBoxBytes = 32 * kBoxCols * 4;
     static constexpr int kStagingOff = kStages * kStageBytes;
-    static constexpr int kBarOff = kStagingOff + kEpiWarps * kBoxBufs * kBoxBytes;
+    // ... and a linear layer's: its columns' bias
+    static constexpr int kBiasBytes = EPI != 0 ? 4 * kEpiCols : 0;
+    static constexpr int kBarOff = kStagingOff + kEpiWarps * (kBoxBufs * kBoxBytes + kBiasBytes);
     static constexpr int kSmemBytes = kBarOff + 256 + 1024;
     static constexpr uint32_t kSfStride = 8 + 8 * NH;     // TMEM scale columns per stage
     static_assert(kStageBytes % 1024 == 0, "stages keep the 1 KB alignment of the swizzle");
@@ -398,7 +400,9 @@ constexpr int kEpiRegs = 216, kEpiRegsOther = 72;
 // (EARLY): all columns are read into registers first and it is released before they
 // are worked on, the registers moving down by 32 from step to step (4608 x 12288 x
 // 3072: 112.6 us with the late release).  Each lane fetches its row's residual a
-// step ahead, the first one before the accumulator is ready, and stores its 64 or
+// step ahead, the first one before the accumulator is ready.  The bias passes through
+// shared memory, fetched a whole tile ahead (from global memory where it is added, it
+// cost BIASGAIN).  A lane stores its 64 or
 // 128 bytes of the row itself, 32 bytes an instruction.  (Boxes in shared memory and
 // TMA stores, as in the plain product, took 28.2 us on 4096 x 4608 x 1152 against
 // 19.9 for the product: a proxy fence and a store per 2 KB.)
@@ -425,9 +429,18 @@ struct LinearEpilogue {
         }
     }
 
-    // x0, row: the first column and this lane's row; taddr: the warp's accumulator,
-    // and the barrier that releases it
-    static __device__ __forceinline__ void run(const GemmArgs &g, int64_t x0, int64_t row,
+    // this lane's part of the bias of columns col ...: those of col + lane + 32 i
+    static __device__ __forceinline__ void fetch_bias(const GemmArgs &g, int64_t col, int lane,
+                                                      float (&b)[COLS / 32])
+    {
+#pragma unroll
+        for (int i = 0; i < COLS / 32; ++i)
+            b[i] = g.epi.bias != nullptr && col + 32 * i + lane < g.n ? __ldg(g.epi.bias + col + 32 * i + lane) : 0.f;
+    }
+
+    // x0, row: the first column and this lane's row; bias: where the columns' bias is in
+    // shared memory; taddr: the warp's accumulator, and the barrier that releases it
+    static __device__ __forceinline__ void run(const GemmArgs &g, int64_t x0, int64_t row, uint32_t bias,
                                                uint32_t taddr, uint32_t release, uint4 (&r)[kChunks])
     {
         const bool f16 = g.epi.fmt == KQ_F16;
@@ -449,19 +462,13 @@ struct LinearEpilogue {
             if (col >= g.n) break;
             const bool inside = col + 32 <= g.n;
             float v[32];
-            if (g.epi.bias != nullptr && inside) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 b = __ldg(reinterpret_cast<const float4 *>(g.epi.bias + col + j));
-                    v[j] = b.x;
-                    v[j + 1] = b.y;
-                    v[j + 2] = b.z;
-                    v[j + 3] = b.w;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    v[j] = g.epi.bias != nullptr && col + j < g.n ? __ldg(g.epi.bias + col + j) : 0.f;
+            for (int j = 0; j < 32; j += 4) {
+                const uint4 b = lds128(bias + 4 * (32 * c + j));
+                v[j] = __uint_as_float(b.x);
+                v[j + 1] = __uint_as_float(b.y);
+                v[j + 2] = __uint_as_float(b.z);
+                v[j + 3] = __uint_as_float(b.w);
             }
             if constexpr (!EARLY) g_wait_ld32(a);
 #pragma unroll
@@ -751,13 +758,26 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
         const uint32_t stg = base + C::kStagingOff +
                              static_cast<uint32_t>(C::kBoxBufs * C::kBoxBytes * (role - 2));
         int64_t tc = 0, nbox = 0;
+        using Epilogue = LinearEpilogue<EPI != 0 ? EPI : 2, C::kEpiCols, C::kAccBufs == 1>;
+        const uint32_t ebias = base + C::kStagingOff + static_cast<uint32_t>(C::kBiasBytes * (role - 2));
+        float nbias[C::kEpiCols / 32];
+        if constexpr (EPI != 0)
+            Epilogue::fetch_bias(g, blockIdx.x % g.ntiles * kXBN + C::kEpiCols * h, lane, nbias);
         for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x, ++tc) {
             const int b = static_cast<int>(tc % C::kAccBufs);
             const int64_t erow = t / g.ntiles * 128 + 32 * qtr + lane;
             const int64_t ecol = t % g.ntiles * kXBN + C::kEpiCols * h;
             uint4 resid[EPI != 0 ? 2 * EPI : 1];
-            using Epilogue = LinearEpilogue<EPI != 0 ? EPI : 2, C::kEpiCols, C::kAccBufs == 1>;
-            if constexpr (EPI != 0) Epilogue::fetch(g, erow, ecol, resid);
+            if constexpr (EPI != 0) {
+                Epilogue::fetch(g, erow, ecol, resid);
+                __syncwarp();                     // the last tile's bias has been read
+#pragma unroll
+                for (int i = 0; i < C::kEpiCols / 32; ++i)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(ebias + 4 * (32 * i + lane)), "f"(nbias[i])
+                                 : "memory");
+                __syncwarp();
+                Epilogue::fetch_bias(g, (t + gridDim.x) % g.ntiles * kXBN + C::kEpiCols * h, lane, nbias);
+            }
             const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full + 8 * b,
                                                               static_cast<uint32_t>((tc / C::kAccBufs) & 1)));
             if (!ok) break;
@@ -765,7 +785,7 @@ __global__ void __launch_bounds__(XCfg<NH, MX, EPI>::kThreads, 1)
             if constexpr (EPI != 0) {
                 const uint32_t acc = tmem_base + (static_cast<uint32_t>(qtr * 32) << 16) +
                                      static_cast<uint32_t>(kXBN * b + C::kEpiCols * h);
-                Epilogue::run(g, ecol, erow, acc, acc_empty + 8 * b, resid);
+                Epilogue::run(g, ecol, erow, ebias, acc, acc_empty + 8 * b, resid);
             } else {
             uint32_t v[128];
             const uint32_t taddr = tmem_base + (static_cast<uint32_t>(qtr * 32) << 16) + 128 * (b + h);
