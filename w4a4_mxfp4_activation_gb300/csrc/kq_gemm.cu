@@ -378,8 +378,9 @@ struct XCfg {
     static constexpr int kBoxBufs = EPI != 0 ? 0 : (NH == 1 ? 2 : 1);
     static constexpr int kBoxBytes = 32 * kBoxCols * 4;
     static constexpr int kStagingOff = kStages * kStageBytes;
-    // ... and a linear layer's: its columns' bias
-    static constexpr int kBiasBytes = EPI != 0 ? 4 * kEpiCols : 0;
+    // ... and a linear layer's: its columns' bias, and for fp32 outputs 32 rows x 64
+    // bytes that turn between registers and stores
+    static constexpr int kBiasBytes = EPI != 0 ? 4 * kEpiCols + (EPI == 4 ? 2048 : 0) : 0;
     static constexpr int kBarOff = kStagingOff + kEpiWarps * (kBoxBufs * kBoxBytes + kBiasBytes);
     static constexpr int kSmemBytes = kBarOff + 256 + 1024;
     static constexpr uint32_t kSfStride = 8 + 8 * NH;     // TMEM scale columns per stage
@@ -401,11 +402,13 @@ constexpr int kEpiRegs = 216, kEpiRegsOther = 72;
 // are worked on, the registers moving down by 32 from step to step (4608 x 12288 x
 // 3072: 112.6 us with the late release).  Each lane fetches its row's residual a
 // step ahead, the first one before the accumulator is ready.  The bias passes through
-// shared memory, fetched a whole tile ahead (from global memory where it is added, it
-// cost BIASGAIN).  A lane stores its 64 or
-// 128 bytes of the row itself, 32 bytes an instruction.  (Boxes in shared memory and
-// TMA stores, as in the plain product, took 28.2 us on 4096 x 4608 x 1152 against
-// 19.9 for the product: a proxy fence and a store per 2 KB.)
+// shared memory, fetched a whole tile ahead: read from global memory where it is added,
+// it cost 2 to 4 us a call (23.1 against 26.3 us on 4096 x 4608 x 1152 with GELU).  A
+// lane stores its 64 bytes of a 16-bit row itself, 32 bytes an instruction (boxes in
+// shared memory and TMA stores, as in the plain product, took 28.2 us there against
+// 19.9 for the product: a proxy fence and a store per 2 KB; a turn through shared memory
+// 25.5); fp32 rows, twice the bytes, are turned to four lanes a row (4608 x 9216 x 3072:
+// 63.4 us against 67.8).
 template <int SIZE, int COLS, bool EARLY>
 struct LinearEpilogue {
     static constexpr int kHeld = EARLY ? COLS : 32;   // columns held in registers
@@ -436,6 +439,33 @@ struct LinearEpilogue {
 #pragma unroll
         for (int i = 0; i < COLS / 32; ++i)
             b[i] = g.epi.bias != nullptr && col + 32 * i + lane < g.n ? __ldg(g.epi.bias + col + 32 * i + lane) : 0.f;
+    }
+
+    // 32 rows x 32 columns of fp32, 16 columns at a time: each lane writes its row's 64
+    // bytes to shared memory (16-byte chunk q of row r at q ^ (r / 2 % 4)), then four
+    // lanes store a row
+    static __device__ __forceinline__ void store_turned(const GemmArgs &g, int64_t col, int64_t row,
+                                                        uint32_t turn, const float (&v)[32])
+    {
+        const int lane = threadIdx.x & 31, r0 = lane >> 2, q0 = lane & 3;
+        const int64_t first = row - lane + r0;
+        uint8_t *const p = static_cast<uint8_t *>(g.epi.out) + (first * g.epi.ldo + col) * 4 + 16 * q0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            __syncwarp();                         // the last half has been read
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                sts128(turn + 64 * lane + ((q ^ (lane >> 1 & 3)) << 4),
+                       make_uint4(__float_as_uint(v[16 * h + 4 * q]), __float_as_uint(v[16 * h + 4 * q + 1]),
+                                  __float_as_uint(v[16 * h + 4 * q + 2]), __float_as_uint(v[16 * h + 4 * q + 3])));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 w = lds128(turn + 64 * (8 * i + r0) + ((q0 ^ (r0 >> 1 & 3)) << 4));
+                if (first + 8 * i < g.m)
+                    *reinterpret_cast<uint4 *>(p + 8 * i * g.epi.ldo * 4 + 64 * h) = w;
+            }
+        }
     }
 
     // x0, row: the first column and this lane's row; bias: where the columns' bias is in
@@ -506,23 +536,27 @@ struct LinearEpilogue {
                     }
                     if (c + 1 < COLS / 32) fetch(g, row, col + 32, r);
                 }
-                uint32_t o[8 * SIZE];
-#pragma unroll
-                for (int j = 0; j < 8 * SIZE; ++j)
-                    o[j] = SIZE == 2 ? pack16(v[2 * j % 32], v[(2 * j + 1) % 32], f16) : __float_as_uint(v[j % 32]);
-                uint8_t *p = out + col * SIZE;
-                if (inside && wide) {
-#pragma unroll
-                    for (int j = 0; j < 8 * SIZE; j += 8) stg256(p + 4 * j, o + j);
-                } else if (inside) {
-#pragma unroll
-                    for (int j = 0; j < 8 * SIZE; j += 4)
-                        *reinterpret_cast<uint4 *>(p + 4 * j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                } else {
+                if (!inside) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
                         if (col + j < g.n) store_out(g.epi.out, row * g.epi.ldo + col + j, g.epi.fmt, v[j]);
+                } else if constexpr (SIZE == 2) {
+                    uint32_t o[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = pack16(v[2 * j], v[2 * j + 1], f16);
+                    if (wide) {
+                        stg256(out + col * 2, o);
+                        stg256(out + col * 2 + 32, o + 8);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            *reinterpret_cast<uint4 *>(out + col * 2 + 4 * j) =
+                                make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    }
                 }
+            }
+            if constexpr (SIZE == 4) {
+                if (inside) store_turned(g, col, row, bias + 4 * COLS, v);
             }
         }
         if constexpr (!EARLY) {
